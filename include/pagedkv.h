@@ -2,8 +2,9 @@
  * pagedkv.h — C ABI of libpagedkv.so: PagedAttention decode on NVIDIA B200
  * (sm_100a), the cache-write scatter, the copy-on-write block copy, and a
  * host-side block allocator with prefix caching; beyond the decode path,
- * chunked-prefill attention, cascade decode over shared prefixes, and an
- * 8-bit (E4M3) cache.
+ * chunked-prefill attention, cascade decode over shared prefixes, an 8-bit
+ * (E4M3) cache, and speculative decoding (attention for a tree of drafted
+ * tokens, their verification, and compaction of the accepted path).
  *
  * Sources cited by page title and section:
  *   [csdn]       devpress.csdn.net, "vLLM镜像深度优化：PagedAttention助力大模型推理效率飞跃"
@@ -69,7 +70,12 @@ typedef enum {
 
 /* PKV_FP8_E4M3 is a cache element type only (copy_blocks, and the caches of
  * the *_fp8 entry points); queries and outputs are always 16-bit. */
-typedef enum { PKV_FP16 = 0, PKV_BF16 = 1, PKV_FP8_E4M3 = 2 } pkv_dtype;
+typedef enum {
+  PKV_FP16 = 0,
+  PKV_BF16 = 1,
+  PKV_FP8_E4M3 = 2,
+  PKV_FP32 = 3 /* probabilities of pkv_verify_draft only */
+} pkv_dtype;
 
 /* Bits ORed into *dev_err by the kernels. */
 #define PKV_DEVERR_BAD_BLOCK 1u   /* decode: table entry outside [0, num_blocks)          */
@@ -81,6 +87,12 @@ typedef enum { PKV_FP16 = 0, PKV_BF16 = 1, PKV_FP8_E4M3 = 2 } pkv_dtype;
 #define PKV_DEVERR_BAD_SCALE 32u  /* *_fp8: a scale that is not finite and > 0            */
 #define PKV_DEVERR_BAD_ORDER 64u  /* *_ordered, *_planned: an entry outside [0, num_seqs),
                                      or a work item that disagrees with the lengths */
+#define PKV_DEVERR_BAD_TREE 128u  /* drafted trees: a parent that does not come before its
+                                     node, or an accepted list that does not rise within
+                                     its tree                                              */
+#define PKV_DEVERR_BAD_DRAFT 256u /* pkv_verify_draft: a drafted token outside
+                                     [0, vocab_size), or weights whose sum is not
+                                     finite and > 0                                        */
 
 /* Library version string, e.g. "pagedkv 0.1.0 sm_100a". */
 const char* pkv_version(void);
@@ -553,6 +565,158 @@ pkv_status pkv_paged_attn_decode_cascade_fp8(
     unsigned* dev_err, void* stream);
 
 /*
+ * Speculative decoding.  A draft proposes a tree of tokens for each sequence;
+ * one pass of the target model scores all of them, a verification keeps one
+ * path of the tree, and the kept tokens' K/V stay in the cache.  Per step and
+ * sequence: reserve q_len slots and write the tree's K/V
+ * (pkv_reshape_and_cache), attend (pkv_paged_attn_tree), verify
+ * (pkv_verify_draft), move the kept K/V together (pkv_compact_accepted) and
+ * give the rejected tokens' blocks back (pkv_alloc_truncate).  The device
+ * calls take one another's outputs, so a step needs no host synchronisation
+ * before its last call.  Not in the source pages, which decode one token per
+ * sequence and step.
+ *
+ * A tree: sequence i's q_len_i = query_start[i+1] - query_start[i] nodes are
+ * its last q_len_i cached tokens, in draft order; context_lens[i] counts them,
+ * so its history is the context_lens[i] - q_len_i tokens before them.
+ * parents[query_start[i] + j] is the index within the tree (0-based) of node
+ * j's parent, which must come before it, or -1 for a child of the history.  A
+ * tree has at most PKV_MAX_TREE_NODES nodes.  A parent outside [-1, j) sets
+ * PKV_DEVERR_BAD_TREE; attention then takes the node for a child of the
+ * history, and verification never reaches it.
+ */
+#define PKV_MAX_TREE_NODES 256
+
+/*
+ * pkv_paged_attn_tree — attention of every node of each sequence's tree over
+ * the history and the node's own ancestors.  With h the history's length, node
+ * j sees keys 0 .. h - 1 and h + a for each a on the path from j up to the
+ * history (j itself among them):
+ *     out[t, n, :] = softmax(scale * q[t, n, :] . K[visible]^T) . V[visible]
+ * with query head n reading kv head n / (num_heads / num_kv_heads).  fp32
+ * accumulation; output rounded to nearest even.  K and V of nodes that a row
+ * does not see do not enter it, whatever they hold (NaN and infinities too).
+ * A chain (parents[j] = j - 1) is pkv_paged_attn_prefill's causal mask; one
+ * node per sequence is pkv_paged_attn_decode.
+ *
+ *   q, out        device [T, num_heads, head_dim], T >= query_start[num_seqs]:
+ *                 the nodes of all sequences, packed in order; rows behind the
+ *                 last sequence are left as they are
+ *   num_tokens    T (the extent of q, out and parents)
+ *   query_start   device int32 [num_seqs + 1], non-decreasing, starting at 0;
+ *                 a sequence may have no nodes
+ *   parents       device int32 [T]
+ *   max_query_len an upper bound of q_len_i (sizes the launch), at most
+ *                 max_context_len; above PKV_MAX_TREE_NODES: PKV_ERR_UNSUPPORTED
+ * A sequence whose q_len is negative, above its context length or above
+ * max_query_len, whose rows leave [0, T), or whose context length is out of
+ * range, sets PKV_DEVERR_BAD_CONTEXT and its rows are left unwritten.  A table
+ * entry outside [0, num_blocks) sets PKV_DEVERR_BAD_BLOCK.  No workspace.
+ *
+ * pkv_paged_attn_tree_fp8 — the same over E4M3 caches (values = codes times the
+ * kv head's k_scales / v_scales entry, as pkv_paged_attn_decode_fp8): bf16
+ * queries are rounded to fp16, magnitudes above 65504 saturating.  Null scale
+ * pointers give PKV_ERR_INVALID_ARG; a scale that is not finite and > 0 sets
+ * PKV_DEVERR_BAD_SCALE.
+ */
+pkv_status pkv_paged_attn_tree(void* out, const void* q, const void* k_cache,
+                               const void* v_cache, const int32_t* block_tables,
+                               const int32_t* context_lens, const int32_t* query_start,
+                               const int32_t* parents, float scale, int num_seqs, int num_tokens,
+                               int num_heads, int num_kv_heads, int head_dim, int block_size,
+                               int max_blocks_per_seq, int max_context_len, int max_query_len,
+                               int num_blocks, pkv_dtype dtype, unsigned* dev_err, void* stream);
+pkv_status pkv_paged_attn_tree_fp8(void* out, const void* q, const void* k_cache,
+                                   const void* v_cache, const int32_t* block_tables,
+                                   const int32_t* context_lens, const int32_t* query_start,
+                                   const int32_t* parents, float scale, const float* k_scales,
+                                   const float* v_scales, int num_seqs, int num_tokens,
+                                   int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                   int max_blocks_per_seq, int max_context_len,
+                                   int max_query_len, int num_blocks, pkv_dtype dtype,
+                                   unsigned* dev_err, void* stream);
+
+/*
+ * pkv_verify_draft — which drafted tokens the target model accepts, and the
+ * token that follows them, from given random numbers (speculative sampling:
+ * the kept tokens are distributed as the target's own samples).  Node 0 of a
+ * tree is its root, the token sampled last, which is always kept; a child of
+ * node n was drawn from the draft's distribution q_n at n, and the target's
+ * distribution after n is p_n.  From cur = 0, r = p_0 and Z = 1, for j = 1, 2,
+ * ... in order, each node with parents[j] = cur is tried: it is kept if
+ *     accept_uniforms[j] * q_cur(x_j) * Z < r(x_j);
+ * then cur = j, r = p_j, Z = 1.  Otherwise r becomes the residual
+ *     r = max(r / Z - q_cur, 0),  Z = sum r.
+ * Without draft probabilities the draft is taken as certain, q_cur = 1 at x_j
+ * and 0 elsewhere: a rejection leaves r(x_j) = 0 and takes its weight off Z (a
+ * token tried twice is rejected the second time).  The next token is the
+ * smallest x with
+ *     sum_{y <= x} r(y) > sample_uniforms[i] * sum r
+ * (the last x with r(x) > 0 if rounding leaves none), with r = p_cur again if
+ * nothing of the residual is left.  Negative and NaN weights count as 0.
+ * Differences and sums are taken in 64 bits.
+ *
+ *   accepted      device int32 [num_seqs, max_query_len], written: the kept
+ *                 nodes of each tree in order, the root first, then -1
+ *   num_accepted  device int32 [num_seqs], written: how many are kept; 0 for a
+ *                 sequence without nodes
+ *   next_token    device int32 [num_seqs], written; -1 for a sequence without
+ *                 nodes
+ *   target_probs  device [T, vocab_size] of type `dtype` (PKV_FP32, PKV_FP16 or
+ *                 PKV_BF16), row t the target's probabilities after node t;
+ *                 rows target_stride elements apart (>= vocab_size).  A row
+ *                 should sum to one up to rounding
+ *   draft_probs   device [T, vocab_size], row t the distribution that the
+ *                 children of node t were drawn from, rows draft_stride apart;
+ *                 or NULL (draft_stride is then ignored)
+ *   draft_tokens  device int32 [T], the token of each node (a root's is not read)
+ *   accept_uniforms  device float [T] in [0, 1); a root's is not read
+ *   sample_uniforms  device float [num_seqs] in [0, 1)
+ * All pointers are aligned to their elements' size; the rows may start at any
+ * element.  A sequence whose q_len is negative or above max_query_len, or
+ * whose rows leave [0, num_tokens), sets PKV_DEVERR_BAD_CONTEXT and is treated
+ * as one without nodes.  A drafted token outside [0, vocab_size) that is tried
+ * sets PKV_DEVERR_BAD_DRAFT and is passed over (r and Z stay); weights whose
+ * sum is not finite and > 0 set the same bit and give next_token = -1.
+ */
+pkv_status pkv_verify_draft(int32_t* accepted, int32_t* num_accepted, int32_t* next_token,
+                            const void* target_probs, int64_t target_stride,
+                            const void* draft_probs, int64_t draft_stride,
+                            const int32_t* draft_tokens, const int32_t* parents,
+                            const int32_t* query_start, const float* accept_uniforms,
+                            const float* sample_uniforms, int num_seqs, int num_tokens,
+                            int max_query_len, int vocab_size, pkv_dtype dtype,
+                            unsigned* dev_err, void* stream);
+
+/*
+ * pkv_compact_accepted — move the K and V of the kept nodes (what
+ * pkv_verify_draft wrote, or any rising list of nodes) to the front of their
+ * tree: with h the history's length,
+ *     K, V of position h + d  <-  K, V of position h + accepted[i, d],
+ * d = 0 .. num_accepted[i] - 1, through the block table, as if every source
+ * were read before any destination is written.  The sequence then caches
+ * h + num_accepted[i] tokens; what the positions behind hold is unspecified.
+ * Bit-exact.  The blocks of a sequence's tree must not be shared with another
+ * sequence (slots reserved by pkv_alloc_append_slot are not).
+ *
+ *   accepted      device int32 [num_seqs, max_query_len]
+ *   num_accepted  device int32 [num_seqs]
+ *   context_lens, query_start  as for the attention: lengths with the tree
+ *   dtype         the cache's element type: PKV_FP16, PKV_BF16 or PKV_FP8_E4M3
+ * Lengths out of range set PKV_DEVERR_BAD_CONTEXT; a num_accepted[i] outside
+ * [0, q_len_i], or a list that does not rise strictly within [0, q_len_i),
+ * sets PKV_DEVERR_BAD_TREE; nothing of that sequence is then moved.  A move
+ * whose table entry is outside [0, num_blocks) sets PKV_DEVERR_BAD_BLOCK and is
+ * skipped.
+ */
+pkv_status pkv_compact_accepted(void* k_cache, void* v_cache, const int32_t* block_tables,
+                                const int32_t* context_lens, const int32_t* query_start,
+                                const int32_t* accepted, const int32_t* num_accepted,
+                                int num_seqs, int max_query_len, int num_kv_heads, int head_dim,
+                                int block_size, int max_blocks_per_seq, int num_blocks,
+                                pkv_dtype dtype, unsigned* dev_err, void* stream);
+
+/*
  * pkv_decode_step_host — one whole decode step from HOST buffers: copies the
  * step's inputs host->device, runs copy_blocks (if num_pairs > 0),
  * reshape_and_cache (if num_new_tokens > 0) and paged_attn_decode, and copies
@@ -669,6 +833,12 @@ pkv_status pkv_alloc_append_slot(pkv_alloc* a, int64_t seq_id, int64_t* slot,
  * unless an error status is returned). */
 pkv_status pkv_alloc_append_slots(pkv_alloc* a, const int64_t* seq_ids, int n, int64_t* slots,
                                   int64_t* cow_pairs, int* num_cow, int* num_done);
+/* Drops a sequence's last tokens, such as rejected drafts, so that the first
+ * num_tokens (0 to its length, else PKV_ERR_INVALID_ARG) remain: the blocks past
+ * ceil(num_tokens / block_size) lose one reference each, front to back, as in
+ * free_seq.  A prefix-cached block that a sequence is cut back into loses its
+ * cache entry when the last holder appends into it. */
+pkv_status pkv_alloc_truncate(pkv_alloc* a, int64_t seq_id, int64_t num_tokens);
 pkv_status pkv_alloc_free_seq(pkv_alloc* a, int64_t seq_id);
 /* table_out: host int32 [n, max_blocks], padded with -1. */
 pkv_status pkv_alloc_block_table(const pkv_alloc* a, const int64_t* seq_ids, int n,

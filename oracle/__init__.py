@@ -23,6 +23,8 @@ Modules:
 * ``dtypes``         exact widening of fp16/bf16 bit patterns to float64
 * ``fp8``            the E4M3 cache: encode / decode, the quantising write,
                      decode and prefill over dequantised codes
+* ``speculative``    attention of drafted trees, their verification, and the
+                     compaction of the accepted path
 """
 
-from . import attention, block_manager, cache_ops, dtypes, fp8  # noqa: F401
+from . import attention, block_manager, cache_ops, dtypes, fp8, speculative  # noqa: F401

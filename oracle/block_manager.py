@@ -167,6 +167,9 @@ class BlockManager:
                 self.refcount[last] -= 1
                 seq["blocks"][-1] = fresh
                 cow_src, cow_dst = last, fresh
+            elif last in self.cache_key:
+                # cut back into a cached block: the append changes its tokens
+                del self.cache[self.cache_key.pop(last)]
         seq["tokens"] = pos + 1
         return seq["blocks"][-1] * self.block_size + offset, cow_src, cow_dst
 
@@ -179,6 +182,16 @@ class BlockManager:
             if src >= 0:
                 pairs.append((src, dst))
         return slots, pairs
+
+    def truncate(self, seq_id, num_tokens):
+        """Keep the first ``num_tokens`` tokens; the blocks behind lose a reference."""
+        if seq_id not in self.seqs or not 0 <= num_tokens <= self.seqs[seq_id]["tokens"]:
+            raise AllocError("INVALID_ARG", "unknown seq id or bad length")
+        seq = self.seqs[seq_id]
+        keep = blocks_for(num_tokens, self.block_size)
+        for b in seq["blocks"][keep:]:
+            self._release(b)
+        seq["blocks"], seq["tokens"] = seq["blocks"][:keep], num_tokens
 
     def free_seq(self, seq_id):
         if seq_id not in self.seqs:

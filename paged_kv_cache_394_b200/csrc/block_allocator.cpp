@@ -66,15 +66,20 @@ struct pkv_alloc {
     } else {
       b = evictable.front();
       evictable.pop_front();
-      CacheEntry& e = entry[b];
-      cache.erase(e.hash);
-      e.cached = false;
-      e.evictable = false;
-      e.tokens.clear();
+      entry[b].evictable = false;
+      uncache(b);
       ++evicted;
     }
     refcount[b] = 1;
     return b;
+  }
+
+  // Drops a cached block's entry.
+  void uncache(int b) {
+    CacheEntry& e = entry[b];
+    cache.erase(e.hash);
+    e.cached = false;
+    e.tokens.clear();
   }
 
   void release(int b) {
@@ -182,6 +187,10 @@ extern "C" pkv_status pkv_alloc_append_slot(pkv_alloc* a, int64_t seq_id, int64_
       s.blocks.back() = fresh;
       src = last;
       dst = fresh;
+    } else if (a->entry[last].cached) {
+      // cut back into a cached block (pkv_alloc_truncate): the append changes
+      // its tokens, so no later prompt may find it
+      a->uncache(last);
     }
   }
   s.tokens = pos + 1;
@@ -213,6 +222,18 @@ extern "C" pkv_status pkv_alloc_append_slots(pkv_alloc* a, const int64_t* seq_id
     }
     if (num_done) *num_done = i + 1;
   }
+  return PKV_OK;
+}
+
+extern "C" pkv_status pkv_alloc_truncate(pkv_alloc* a, int64_t seq_id, int64_t num_tokens) {
+  if (a == nullptr || num_tokens < 0) return PKV_ERR_INVALID_ARG;
+  auto it = a->seqs.find(seq_id);
+  if (it == a->seqs.end() || num_tokens > it->second.tokens) return PKV_ERR_INVALID_ARG;
+  pkv_alloc::Seq& s = it->second;
+  const size_t keep = static_cast<size_t>(blocks_for(num_tokens, a->block_size));
+  for (size_t k = keep; k < s.blocks.size(); ++k) a->release(s.blocks[k]);
+  s.blocks.resize(keep);
+  s.tokens = num_tokens;
   return PKV_OK;
 }
 

@@ -20,9 +20,11 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_OUT_OF_BLOCKS = range(6)
-FP16, BF16, FP8_E4M3 = 0, 1, 2
+FP16, BF16, FP8_E4M3, FP32 = 0, 1, 2, 3
 (DEVERR_BAD_BLOCK, DEVERR_BAD_SLOT, DEVERR_BAD_PAIR, DEVERR_BAD_CONTEXT, DEVERR_TIMEOUT,
- DEVERR_BAD_SCALE, DEVERR_BAD_ORDER) = (1, 2, 4, 8, 16, 32, 64)
+ DEVERR_BAD_SCALE, DEVERR_BAD_ORDER, DEVERR_BAD_TREE, DEVERR_BAD_DRAFT) = (
+     1, 2, 4, 8, 16, 32, 64, 128, 256)
+MAX_TREE_NODES = 256
 
 _vp, _i, _i64, _f, _sz, _u = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float,
                               ctypes.c_size_t, ctypes.c_uint)
@@ -95,6 +97,15 @@ _paged_attn_prefill_fp8_planned = _proto("pkv_paged_attn_prefill_fp8_planned", _
                                          _vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _f, _vp, _vp, _i,
                                          _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _sz, _vp,
                                          _vp)
+_paged_attn_tree = _proto("pkv_paged_attn_tree", _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _f,
+                          _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _vp)
+_paged_attn_tree_fp8 = _proto("pkv_paged_attn_tree_fp8", _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                              _vp, _f, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp,
+                              _vp)
+_verify_draft = _proto("pkv_verify_draft", _i, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                       _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp)
+_compact_accepted = _proto("pkv_compact_accepted", _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i,
+                           _i, _i, _i, _i, _i, _i, _vp, _vp)
 _testing_decode_wait = _proto("pkv_testing_decode_wait", _i, ctypes.c_uint64, _i)
 _pipeline_staging_bytes = _proto("pkv_decode_pipeline_staging_bytes", _sz, _i, _i, _i, _i, _i, _i,
                                  _i)
@@ -111,6 +122,7 @@ _alloc_add_seq = _proto("pkv_alloc_add_seq", _i, _vp, _i64, _i64)
 _alloc_fork = _proto("pkv_alloc_fork", _i, _vp, _i64, _i64)
 _alloc_append_slot = _proto("pkv_alloc_append_slot", _i, _vp, _i64, _vp, _vp, _vp)
 _alloc_append_slots = _proto("pkv_alloc_append_slots", _i, _vp, _vp, _i, _vp, _vp, _vp, _vp)
+_alloc_truncate = _proto("pkv_alloc_truncate", _i, _vp, _i64, _i64)
 _alloc_free_seq = _proto("pkv_alloc_free_seq", _i, _vp, _i64)
 _alloc_block_table = _proto("pkv_alloc_block_table", _i, _vp, _vp, _i, _i, _vp)
 _alloc_context_lens = _proto("pkv_alloc_context_lens", _i, _vp, _vp, _i, _vp)
@@ -643,6 +655,159 @@ def paged_attn_prefill_fp8(out, q, k_cache, v_cache, block_tables, context_lens,
            "paged_attn_prefill_fp8")
 
 
+def _same_device(*tensors):
+    """All tensors (Nones left out) on the calling thread's current device."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != here:
+            raise ValueError("all tensors must be on the current CUDA device (%d)" % here)
+
+
+def _tree_args(out, q, k_cache, v_cache, block_tables, context_lens, query_start, parents,
+               num_kv_heads, block_size, dev_err):
+    for n, t in (("out", out), ("q", q), ("k_cache", k_cache), ("v_cache", v_cache)):
+        _dev(t, n)
+    for n, t in (("block_tables", block_tables), ("context_lens", context_lens),
+                 ("query_start", query_start), ("parents", parents)):
+        _dev(t, n, torch.int32)
+    _same_device(out, q, k_cache, v_cache, block_tables, context_lens, query_start, parents,
+                 dev_err)
+    t, h, d = q.shape
+    num_blocks, hkv, bs, dk = k_cache.shape
+    s = context_lens.shape[0]
+    if ((hkv, bs, dk) != (num_kv_heads, block_size, d) or out.shape != q.shape
+            or v_cache.shape != k_cache.shape):
+        raise ValueError("shape mismatch")
+    if (query_start.shape != (s + 1,) or block_tables.dim() != 2 or block_tables.shape[0] != s
+            or parents.shape != (t,)):
+        raise ValueError("query_start must be [S+1], block_tables [S, max_blocks], parents [T]")
+    if out.dtype != q.dtype or v_cache.dtype != k_cache.dtype:
+        raise TypeError("q and out, and the two caches, must share a dtype")
+    return s, t, h, d, num_blocks
+
+
+def paged_attn_tree(out, q, k_cache, v_cache, block_tables, context_lens, query_start, parents,
+                    scale, num_kv_heads, block_size, max_context_len, max_query_len, dev_err=None,
+                    stream=None):
+    """Attention of each sequence's tree of drafted tokens: a node sees the
+    history and its own ancestors.  q/out are [T, H, D] (the nodes packed by
+    sequence), query_start [S+1], parents int32 [T] (index within the tree, -1
+    for a child of the history).  See include/pagedkv.h."""
+    s, t, h, d, num_blocks = _tree_args(out, q, k_cache, v_cache, block_tables, context_lens,
+                                        query_start, parents, num_kv_heads, block_size, dev_err)
+    if q.dtype != k_cache.dtype:
+        raise TypeError("q, out and caches must share a dtype")
+    _check(_paged_attn_tree(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+                            _ptr(context_lens), _ptr(query_start), _ptr(parents), float(scale), s,
+                            t, h, num_kv_heads, d, block_size, block_tables.shape[1],
+                            max_context_len, max_query_len, num_blocks, _dtype_code(q),
+                            _ptr(dev_err), _stream(stream)),
+           "paged_attn_tree")
+
+
+def paged_attn_tree_fp8(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
+                        parents, scale, k_scales, v_scales, num_kv_heads, block_size,
+                        max_context_len, max_query_len, dev_err=None, stream=None):
+    """paged_attn_tree over E4M3 caches (values = code * scale of the kv head);
+    q and out are 16-bit.  See include/pagedkv.h."""
+    s, t, h, d, num_blocks = _tree_args(out, q, k_cache, v_cache, block_tables, context_lens,
+                                        query_start, parents, num_kv_heads, block_size, dev_err)
+    if _cache_dtype_code(k_cache) != FP8_E4M3:
+        raise TypeError("E4M3 caches must be uint8 (or float8_e4m3fn)")
+    ks, vs = _scales_for(k_scales, v_scales, num_kv_heads, q.device, stream)
+    _same_device(ks, vs)
+    _check(_paged_attn_tree_fp8(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                _ptr(block_tables), _ptr(context_lens), _ptr(query_start),
+                                _ptr(parents), float(scale), _ptr(ks), _ptr(vs), s, t, h,
+                                num_kv_heads, d, block_size, block_tables.shape[1],
+                                max_context_len, max_query_len, num_blocks, _dtype_code(q),
+                                _ptr(dev_err), _stream(stream)),
+           "paged_attn_tree_fp8")
+
+
+def _prob_rows(t, name, rows, vocab, dtype):
+    """[T, V] probabilities: unit stride along the vocabulary, rows any distance apart."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != (rows, vocab):
+        raise ValueError("%s must be [T, vocab]" % name)
+    if vocab > 1 and t.stride(1) != 1:
+        raise ValueError("%s must be contiguous along the vocabulary" % name)
+    if rows <= 1:
+        return vocab
+    if t.stride(0) < vocab:
+        raise ValueError("%s must not have overlapping rows" % name)
+    return t.stride(0)
+
+
+def verify_draft(accepted, num_accepted, next_token, target_probs, draft_tokens, parents,
+                 query_start, accept_uniforms, sample_uniforms, max_query_len, draft_probs=None,
+                 dev_err=None, stream=None):
+    """Verify each sequence's drafted tree against the target's probabilities
+    [T, V] (float32, float16 or bfloat16): writes the kept nodes into accepted
+    [S, max_query_len] (-1 behind them), their count into num_accepted [S] and
+    the token that follows into next_token [S].  draft_probs [T, V] are the
+    distributions the children were drawn from; None takes the draft as
+    certain of its tokens.  See include/pagedkv.h."""
+    for n, t in (("accepted", accepted), ("num_accepted", num_accepted),
+                 ("next_token", next_token), ("draft_tokens", draft_tokens),
+                 ("parents", parents), ("query_start", query_start)):
+        _dev(t, n, torch.int32)
+    _dev(accept_uniforms, "accept_uniforms", torch.float32)
+    _dev(sample_uniforms, "sample_uniforms", torch.float32)
+    _same_device(accepted, num_accepted, next_token, target_probs, draft_tokens, parents,
+                 query_start, accept_uniforms, sample_uniforms, draft_probs, dev_err)
+    if target_probs.dim() != 2:
+        raise ValueError("target_probs must be [T, vocab]")
+    t, v = target_probs.shape
+    s = num_accepted.shape[0]
+    code = FP32 if target_probs.dtype == torch.float32 else _dtype_code(target_probs)
+    if (query_start.shape != (s + 1,) or next_token.shape != (s,) or sample_uniforms.shape != (s,)
+            or accepted.shape != (s, max_query_len)):
+        raise ValueError("query_start must be [S+1], num_accepted, next_token and "
+                         "sample_uniforms [S], accepted [S, max_query_len]")
+    if draft_tokens.shape != (t,) or parents.shape != (t,) or accept_uniforms.shape != (t,):
+        raise ValueError("draft_tokens, parents and accept_uniforms must be [T]")
+    stride = _prob_rows(target_probs, "target_probs", t, v, target_probs.dtype)
+    dstride = (_prob_rows(draft_probs, "draft_probs", t, v, target_probs.dtype)
+               if draft_probs is not None else 0)
+    _check(_verify_draft(_ptr(accepted), _ptr(num_accepted), _ptr(next_token), _ptr(target_probs),
+                         stride, _ptr(draft_probs), dstride, _ptr(draft_tokens), _ptr(parents),
+                         _ptr(query_start), _ptr(accept_uniforms), _ptr(sample_uniforms), s, t,
+                         max_query_len, v, code, _ptr(dev_err), _stream(stream)),
+           "verify_draft")
+
+
+def compact_accepted(k_cache, v_cache, block_tables, context_lens, query_start, accepted,
+                     num_accepted, dev_err=None, stream=None):
+    """Move the K/V of each tree's kept nodes (accepted [S, max_query_len] and
+    num_accepted [S], as verify_draft writes them) to the front of the tree's
+    cache positions, in place.  16-bit or E4M3 caches.  See include/pagedkv.h."""
+    _dev(k_cache, "k_cache")
+    _dev(v_cache, "v_cache")
+    for n, t in (("block_tables", block_tables), ("context_lens", context_lens),
+                 ("query_start", query_start), ("accepted", accepted),
+                 ("num_accepted", num_accepted)):
+        _dev(t, n, torch.int32)
+    _same_device(k_cache, v_cache, block_tables, context_lens, query_start, accepted,
+                 num_accepted, dev_err)
+    if v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must match")
+    num_blocks, hkv, bs, d = k_cache.shape
+    s = context_lens.shape[0]
+    if (query_start.shape != (s + 1,) or block_tables.dim() != 2 or block_tables.shape[0] != s
+            or accepted.dim() != 2 or accepted.shape[0] != s or num_accepted.shape != (s,)):
+        raise ValueError("query_start must be [S+1], block_tables [S, max_blocks], "
+                         "accepted [S, max_query_len], num_accepted [S]")
+    _check(_compact_accepted(_ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
+                             _ptr(query_start), _ptr(accepted), _ptr(num_accepted), s,
+                             accepted.shape[1], hkv, d, bs, block_tables.shape[1], num_blocks,
+                             _cache_dtype_code(k_cache), _ptr(dev_err), _stream(stream)),
+           "compact_accepted")
+
+
 def testing_decode_wait(wait_ns, withhold_first_load=False):
     """Testing hook: the decode kernels' bound on a wait for their own loads,
     and whether the first CTA withholds its first load so that the wait runs
@@ -804,6 +969,10 @@ class BlockAllocator:
         _check(_alloc_append_slots(self._h, ids, n, slots, pairs, ctypes.byref(ncow),
                                    ctypes.byref(done)), "append_slots")
         return list(slots[:n]), [(pairs[2 * k], pairs[2 * k + 1]) for k in range(ncow.value)]
+
+    def truncate(self, seq_id, num_tokens):
+        """Keep a sequence's first num_tokens tokens; the blocks behind are released."""
+        _check(_alloc_truncate(self._h, seq_id, num_tokens), "truncate")
 
     def free_seq(self, seq_id):
         _check(_alloc_free_seq(self._h, seq_id), "free_seq")
