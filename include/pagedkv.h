@@ -611,7 +611,13 @@ pkv_status pkv_paged_attn_decode_cascade_fp8(
  * A sequence whose q_len is negative, above its context length or above
  * max_query_len, whose rows leave [0, T), or whose context length is out of
  * range, sets PKV_DEVERR_BAD_CONTEXT and its rows are left unwritten.  A table
- * entry outside [0, num_blocks) sets PKV_DEVERR_BAD_BLOCK.  No workspace.
+ * entry outside [0, num_blocks) sets PKV_DEVERR_BAD_BLOCK.
+ *
+ *   workspace     device scratch, 16-byte aligned, of at least
+ *                 pkv_paged_attn_tree_workspace_bytes(...) bytes for the same
+ *                 shape (less, or none: PKV_ERR_WORKSPACE).  It needs no
+ *                 preparation and holds nothing afterwards; calls that may run
+ *                 at the same time need one each.
  *
  * pkv_paged_attn_tree_fp8 — the same over E4M3 caches (values = codes times the
  * kv head's k_scales / v_scales entry, as pkv_paged_attn_decode_fp8): bf16
@@ -619,13 +625,16 @@ pkv_status pkv_paged_attn_decode_cascade_fp8(
  * pointers give PKV_ERR_INVALID_ARG; a scale that is not finite and > 0 sets
  * PKV_DEVERR_BAD_SCALE.
  */
+size_t pkv_paged_attn_tree_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads,
+                                           int head_dim, int max_context_len, int max_query_len);
 pkv_status pkv_paged_attn_tree(void* out, const void* q, const void* k_cache,
                                const void* v_cache, const int32_t* block_tables,
                                const int32_t* context_lens, const int32_t* query_start,
                                const int32_t* parents, float scale, int num_seqs, int num_tokens,
                                int num_heads, int num_kv_heads, int head_dim, int block_size,
                                int max_blocks_per_seq, int max_context_len, int max_query_len,
-                               int num_blocks, pkv_dtype dtype, unsigned* dev_err, void* stream);
+                               int num_blocks, pkv_dtype dtype, void* workspace,
+                               size_t workspace_bytes, unsigned* dev_err, void* stream);
 pkv_status pkv_paged_attn_tree_fp8(void* out, const void* q, const void* k_cache,
                                    const void* v_cache, const int32_t* block_tables,
                                    const int32_t* context_lens, const int32_t* query_start,
@@ -634,7 +643,7 @@ pkv_status pkv_paged_attn_tree_fp8(void* out, const void* q, const void* k_cache
                                    int num_heads, int num_kv_heads, int head_dim, int block_size,
                                    int max_blocks_per_seq, int max_context_len,
                                    int max_query_len, int num_blocks, pkv_dtype dtype,
-                                   unsigned* dev_err, void* stream);
+                                   void* workspace, size_t workspace_bytes, unsigned* dev_err, void* stream);
 
 /*
  * pkv_verify_draft — which drafted tokens the target model accepts, and the

@@ -29,19 +29,25 @@ inline cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 // scheduled while the previous kernel in the stream drains, so the kernel
 // must call griddepcontrol.wait before it touches memory that kernel uses.
 template <class... KArgs, class... Args>
-cudaError_t launch_after_previous(void (*kernel)(KArgs...), dim3 grid, dim3 block, void* stream,
-                                  Args&&... args) {
+cudaError_t launch_after_previous_smem(void (*kernel)(KArgs...), dim3 grid, dim3 block,
+                                       size_t smem_bytes, void* stream, Args&&... args) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
-  cfg.dynamicSmemBytes = 0;
+  cfg.dynamicSmemBytes = smem_bytes;
   cfg.stream = as_stream(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+template <class... KArgs, class... Args>
+cudaError_t launch_after_previous(void (*kernel)(KArgs...), dim3 grid, dim3 block, void* stream,
+                                  Args&&... args) {
+  return launch_after_previous_smem(kernel, grid, block, 0, stream, std::forward<Args>(args)...);
 }
 
 // 2-D TMA tensor map over a cache viewed as [num_blocks * hkv * bs, d] rows

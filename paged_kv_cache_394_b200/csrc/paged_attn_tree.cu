@@ -1,7 +1,8 @@
 // paged_attn_tree.cu — host side of tree attention: validation, dispatch and
-// the C entry points.  The kernel is in paged_attn_tree_kernels.cuh.
+// the C entry points.  The kernels are in paged_attn_tree_kernels.cuh.
 #include <math.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "host_common.h"
@@ -10,12 +11,56 @@
 namespace pkv {
 namespace {
 
-using TreeFn = void (*)(const TreeParams);
+using TreeFn = void (*)(const TreeParams, const CUtensorMap, const CUtensorMap);
+using TreeMergeFn = void (*)(const TreeParams);
 
-template <class DT, class CT>
-TreeFn tree_fn(int head_dim) {
-  return head_dim == 128 ? paged_attn_tree_kernel<128, DT, CT>
-                         : paged_attn_tree_kernel<64, DT, CT>;
+struct TreeEntry {
+  TreeFn fn;
+  TreeMergeFn merge;
+  size_t smem;
+  int threads, rows, ctas;  // ctas: those resident at once
+};
+
+constexpr int kSms = 148;
+
+template <int D, class DT, bool FP8, int QT>
+TreeEntry tree_entry() {
+  using Tr = TreeTraits<D, DT, FP8, QT>;
+  return {paged_attn_tree_kernel<Tr>, paged_attn_tree_merge_kernel<D, Tr::ROWS, DT>,
+          Tr::smem_bytes(), Tr::THREADS, Tr::ROWS, kSms * Tr::MIN_BLOCKS};
+}
+
+template <int D, class DT>
+TreeEntry tree_entry(bool fp8, int qt) {
+  if (qt == 1) return fp8 ? tree_entry<D, DT, true, 1>() : tree_entry<D, DT, false, 1>();
+  return fp8 ? tree_entry<D, DT, true, 2>() : tree_entry<D, DT, false, 2>();
+}
+
+// Two query tiles a CTA once a unit can have more than 128 rows: they share
+// each K/V tile.
+TreeEntry tree_entry(int head_dim, pkv_dtype dt, bool fp8, int max_rows) {
+  const int qt = max_rows > 128 ? 2 : 1;
+  if (head_dim == 128)
+    return dt == PKV_FP16 ? tree_entry<128, Fp16>(fp8, qt) : tree_entry<128, Bf16>(fp8, qt);
+  return dt == PKV_FP16 ? tree_entry<64, Fp16>(fp8, qt) : tree_entry<64, Bf16>(fp8, qt);
+}
+
+// CTAs of a launch: no more than are resident, nor than the longest batch
+// within the bounds has stretches of kTreeMinTiles.
+int tree_ctas(int resident, int rows, int num_seqs, int group, int num_kv_heads,
+              int max_context_len, int max_query_len) {
+  const long long tiles = (max_context_len + kTreeKeys - 1) / kTreeKeys + kTreeUnitCost;
+  const long long units =
+      static_cast<long long>(num_seqs) * ((max_query_len * group + rows - 1) / rows);
+  // units * kv heads * tiles, without its overflow
+  if (units >= resident || units * num_kv_heads >= resident) return resident;
+  const long long most = (units * num_kv_heads * tiles + kTreeMinTiles - 1) / kTreeMinTiles;
+  return static_cast<int>(std::min<long long>(resident, most));
+}
+
+size_t tree_ws_bytes(int ctas, int rows, int head_dim) {
+  return static_cast<size_t>(ctas) *
+         (sizeof(int4) + 2 * static_cast<size_t>(rows) * (8 + 4 * static_cast<size_t>(head_dim)));
 }
 
 // Validates and launches; fp8: the caches hold E4M3 codes with per-kv-head
@@ -26,8 +71,8 @@ pkv_status tree_launch(void* out, const void* q, const void* k_cache, const void
                        int num_seqs, int num_tokens, int num_heads, int num_kv_heads,
                        int head_dim, int block_size, int max_blocks_per_seq, int max_context_len,
                        int max_query_len, int num_blocks, pkv_dtype dtype, bool fp8,
-                       const float* k_scales, const float* v_scales, unsigned* dev_err,
-                       void* stream) {
+                       const float* k_scales, const float* v_scales, void* workspace,
+                       size_t workspace_bytes, unsigned* dev_err, void* stream) {
   if (num_seqs < 0 || num_tokens < 0 || num_heads <= 0 || num_kv_heads <= 0 ||
       max_blocks_per_seq <= 0 || max_context_len < 0 || max_query_len < 0 || num_blocks <= 0 ||
       !dtype_valid(dtype) || num_heads % num_kv_heads != 0 || !isfinite(scale) ||
@@ -48,9 +93,19 @@ pkv_status tree_launch(void* out, const void* q, const void* k_cache, const void
     return PKV_ERR_INVALID_ARG;
   if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
     return PKV_ERR_INVALID_ARG;
-  const long long grid =
-      (static_cast<long long>(num_seqs) * max_query_len * num_heads + 3) / 4;
-  if (grid > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+  const int max_rows = max_query_len * group;
+  const TreeEntry e = tree_entry(head_dim, dtype, fp8, max_rows);
+  const int ctas = tree_ctas(e.ctas, e.rows, num_seqs, group, num_kv_heads, max_context_len,
+                             max_query_len);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < tree_ws_bytes(ctas, e.rows, head_dim))
+    return PKV_ERR_WORKSPACE;
+  const pkv_dtype cdt = fp8 ? PKV_FP8_E4M3 : dtype;
+  CUtensorMap kmap, vmap;
+  pkv_status st =
+      cache_tensor_map(&kmap, k_cache, num_blocks, num_kv_heads, block_size, head_dim, cdt);
+  if (st != PKV_OK) return st;
+  st = cache_tensor_map(&vmap, v_cache, num_blocks, num_kv_heads, block_size, head_dim, cdt);
+  if (st != PKV_OK) return st;
   TreeParams p = {};
   p.out = out;
   p.q = q;
@@ -67,33 +122,56 @@ pkv_status tree_launch(void* out, const void* q, const void* k_cache, const void
   p.num_tokens = num_tokens;
   p.num_heads = num_heads;
   p.num_kv_heads = num_kv_heads;
+  p.group_shift = group == 1 ? 0 : group == 2 ? 1 : group == 4 ? 2 : 3;
   p.block_size = block_size;
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.max_context_len = max_context_len;
   p.max_query_len = max_query_len;
   p.num_blocks = num_blocks;
   p.err = dev_err;
-  const TreeFn fn = dtype == PKV_FP16 ? (fp8 ? tree_fn<Fp16, Fp8E4M3>(head_dim)
-                                             : tree_fn<Fp16, Fp16>(head_dim))
-                                      : (fp8 ? tree_fn<Bf16, Fp8E4M3>(head_dim)
-                                             : tree_fn<Bf16, Bf16>(head_dim));
-  fn<<<static_cast<unsigned>(grid), 128, 0, as_stream(stream)>>>(p);
-  return cuda_status(cudaGetLastError());
+  p.ws_meta = static_cast<int4*>(workspace);
+  p.ws_o = reinterpret_cast<float*>(p.ws_meta + ctas);
+  p.ws_ml = reinterpret_cast<float2*>(p.ws_o + static_cast<size_t>(ctas) * 2 * e.rows * head_dim);
+  st = cuda_status(cudaFuncSetAttribute(e.fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(e.smem)));
+  if (st != PKV_OK) return st;
+  st = cuda_status(launch_after_previous_smem(e.fn, dim3(ctas), dim3(e.threads), e.smem, stream, p,
+                                              kmap, vmap));
+  if (st != PKV_OK || ctas == 1) return st;
+  const dim3 merge(ctas, (std::min(max_rows, e.rows) + 7) / 8);
+  return cuda_status(launch_after_previous(e.merge, merge, dim3(256), stream, p));
 }
 
 }  // namespace
 }  // namespace pkv
+
+extern "C" size_t pkv_paged_attn_tree_workspace_bytes(int num_seqs, int num_heads,
+                                                      int num_kv_heads, int head_dim,
+                                                      int max_context_len, int max_query_len) {
+  using namespace pkv;
+  if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 ||
+      !head_dim_supported(head_dim) || max_context_len <= 0 || max_query_len <= 0 ||
+      max_query_len > PKV_MAX_TREE_NODES || max_query_len > max_context_len)
+    return 0;
+  const int group = num_heads / num_kv_heads;
+  if (group > 8) return 0;
+  const TreeEntry e = tree_entry(head_dim, PKV_FP16, false, max_query_len * group);
+  return tree_ws_bytes(tree_ctas(e.ctas, e.rows, num_seqs, group, num_kv_heads, max_context_len,
+                                 max_query_len), e.rows, head_dim);
+}
 
 extern "C" pkv_status pkv_paged_attn_tree(
     void* out, const void* q, const void* k_cache, const void* v_cache,
     const int32_t* block_tables, const int32_t* context_lens, const int32_t* query_start,
     const int32_t* parents, float scale, int num_seqs, int num_tokens, int num_heads,
     int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int max_context_len,
-    int max_query_len, int num_blocks, pkv_dtype dtype, unsigned* dev_err, void* stream) {
+    int max_query_len, int num_blocks, pkv_dtype dtype, void* workspace, size_t workspace_bytes,
+    unsigned* dev_err, void* stream) {
   return pkv::tree_launch(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
                           parents, scale, num_seqs, num_tokens, num_heads, num_kv_heads, head_dim,
                           block_size, max_blocks_per_seq, max_context_len, max_query_len,
-                          num_blocks, dtype, false, nullptr, nullptr, dev_err, stream);
+                          num_blocks, dtype, false, nullptr, nullptr, workspace,
+                          workspace_bytes, dev_err, stream);
 }
 
 extern "C" pkv_status pkv_paged_attn_tree_fp8(
@@ -102,9 +180,10 @@ extern "C" pkv_status pkv_paged_attn_tree_fp8(
     const int32_t* parents, float scale, const float* k_scales, const float* v_scales,
     int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size,
     int max_blocks_per_seq, int max_context_len, int max_query_len, int num_blocks,
-    pkv_dtype dtype, unsigned* dev_err, void* stream) {
+    pkv_dtype dtype, void* workspace, size_t workspace_bytes, unsigned* dev_err, void* stream) {
   return pkv::tree_launch(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
                           parents, scale, num_seqs, num_tokens, num_heads, num_kv_heads, head_dim,
                           block_size, max_blocks_per_seq, max_context_len, max_query_len,
-                          num_blocks, dtype, true, k_scales, v_scales, dev_err, stream);
+                          num_blocks, dtype, true, k_scales, v_scales, workspace,
+                          workspace_bytes, dev_err, stream);
 }

@@ -98,10 +98,11 @@ _paged_attn_prefill_fp8_planned = _proto("pkv_paged_attn_prefill_fp8_planned", _
                                          _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _sz, _vp,
                                          _vp)
 _paged_attn_tree = _proto("pkv_paged_attn_tree", _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _f,
-                          _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _vp)
+                          _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _sz, _vp, _vp)
 _paged_attn_tree_fp8 = _proto("pkv_paged_attn_tree_fp8", _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                               _vp, _f, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp,
-                              _vp)
+                              _sz, _vp, _vp)
+_tree_workspace_bytes = _proto("pkv_paged_attn_tree_workspace_bytes", _sz, _i, _i, _i, _i, _i, _i)
 _verify_draft = _proto("pkv_verify_draft", _i, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
                        _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp)
 _compact_accepted = _proto("pkv_compact_accepted", _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i,
@@ -686,28 +687,54 @@ def _tree_args(out, q, k_cache, v_cache, block_tables, context_lens, query_start
     return s, t, h, d, num_blocks
 
 
+def tree_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len,
+                         max_query_len):
+    """Scratch bytes paged_attn_tree and paged_attn_tree_fp8 need for this shape."""
+    return _tree_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len,
+                                 max_query_len)
+
+
+def _tree_workspace(workspace, s, h, hkv, d, max_context_len, max_query_len, device, stream):
+    """(the workspace, its bytes); allocated if None."""
+    if workspace is None:
+        need = _tree_workspace_bytes(s, h, hkv, d, max_context_len, max_query_len)
+        if not need:
+            return None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        if stream is not None:
+            workspace.record_stream(stream)   # the temporary must outlive the launch
+        return workspace, need
+    _dev(workspace, "workspace")
+    _same_device(workspace)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
 def paged_attn_tree(out, q, k_cache, v_cache, block_tables, context_lens, query_start, parents,
                     scale, num_kv_heads, block_size, max_context_len, max_query_len, dev_err=None,
-                    stream=None):
+                    stream=None, workspace=None):
     """Attention of each sequence's tree of drafted tokens: a node sees the
     history and its own ancestors.  q/out are [T, H, D] (the nodes packed by
     sequence), query_start [S+1], parents int32 [T] (index within the tree, -1
-    for a child of the history).  See include/pagedkv.h."""
+    for a child of the history); ``workspace`` is allocated if None.  See
+    include/pagedkv.h."""
     s, t, h, d, num_blocks = _tree_args(out, q, k_cache, v_cache, block_tables, context_lens,
                                         query_start, parents, num_kv_heads, block_size, dev_err)
     if q.dtype != k_cache.dtype:
         raise TypeError("q, out and caches must share a dtype")
+    ws, ws_bytes = _tree_workspace(workspace, s, h, num_kv_heads, d, max_context_len,
+                                   max_query_len, q.device, stream)
     _check(_paged_attn_tree(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                             _ptr(context_lens), _ptr(query_start), _ptr(parents), float(scale), s,
                             t, h, num_kv_heads, d, block_size, block_tables.shape[1],
                             max_context_len, max_query_len, num_blocks, _dtype_code(q),
-                            _ptr(dev_err), _stream(stream)),
+                            _ptr(ws), ws_bytes, _ptr(dev_err), _stream(stream)),
            "paged_attn_tree")
 
 
 def paged_attn_tree_fp8(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
                         parents, scale, k_scales, v_scales, num_kv_heads, block_size,
-                        max_context_len, max_query_len, dev_err=None, stream=None):
+                        max_context_len, max_query_len, dev_err=None, stream=None,
+                        workspace=None):
     """paged_attn_tree over E4M3 caches (values = code * scale of the kv head);
     q and out are 16-bit.  See include/pagedkv.h."""
     s, t, h, d, num_blocks = _tree_args(out, q, k_cache, v_cache, block_tables, context_lens,
@@ -716,12 +743,14 @@ def paged_attn_tree_fp8(out, q, k_cache, v_cache, block_tables, context_lens, qu
         raise TypeError("E4M3 caches must be uint8 (or float8_e4m3fn)")
     ks, vs = _scales_for(k_scales, v_scales, num_kv_heads, q.device, stream)
     _same_device(ks, vs)
+    ws, ws_bytes = _tree_workspace(workspace, s, h, num_kv_heads, d, max_context_len,
+                                   max_query_len, q.device, stream)
     _check(_paged_attn_tree_fp8(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                 _ptr(block_tables), _ptr(context_lens), _ptr(query_start),
                                 _ptr(parents), float(scale), _ptr(ks), _ptr(vs), s, t, h,
                                 num_kv_heads, d, block_size, block_tables.shape[1],
                                 max_context_len, max_query_len, num_blocks, _dtype_code(q),
-                                _ptr(dev_err), _stream(stream)),
+                                _ptr(ws), ws_bytes, _ptr(dev_err), _stream(stream)),
            "paged_attn_tree_fp8")
 
 

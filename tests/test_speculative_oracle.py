@@ -258,7 +258,7 @@ GOOD, BAD = ctypes.c_void_p(0x1000), ctypes.c_void_p(0x1008)
 def tree_call(pk, fp8=False, **over):
     a = dict(out=GOOD, q=GOOD, k=GOOD, v=GOOD, tables=GOOD, lens=GOOD, qs=GOOD, parents=GOOD,
              scale=1.0, ks=GOOD, vs=GOOD, num_seqs=2, num_tokens=8, heads=8, kv=2, d=128, bs=16,
-             mb=8, mctx=100, mq=4, nb=20, dt=0, err=None, stream=None)
+             mb=8, mctx=100, mq=4, nb=20, dt=0, ws=GOOD, ws_bytes=1 << 40, err=None, stream=None)
     a.update(over)
     if not fp8:
         a.pop("ks"), a.pop("vs")
@@ -282,6 +282,10 @@ def test_tree_refusals(pk, fp8):
         assert tree_call(pk, fp8, **over) == uns, over
     for over in (dict(num_seqs=0), dict(num_tokens=0), dict(mq=0)):
         assert tree_call(pk, fp8, **over) == pk.OK, over
+    need = pk.tree_workspace_bytes(2, 8, 2, 128, 100, 4)
+    assert need > 0
+    for over in (dict(ws=None), dict(ws=BAD), dict(ws_bytes=0), dict(ws_bytes=16)):
+        assert tree_call(pk, fp8, **over) == pk.ERR_WORKSPACE, over
     if fp8:
         assert tree_call(pk, True, ks=None) == inv and tree_call(pk, True, vs=None) == inv
 
