@@ -138,8 +138,9 @@ pkv_status tree_launch(void* out, const void* q, const void* k_cache, const void
   st = cuda_status(launch_after_previous_smem(e.fn, dim3(ctas), dim3(e.threads), e.smem, stream, p,
                                               kmap, vmap));
   if (st != PKV_OK || ctas == 1) return st;
-  const dim3 merge(ctas, (std::min(max_rows, e.rows) + 7) / 8);
-  return cuda_status(launch_after_previous(e.merge, merge, dim3(256), stream, p));
+  const dim3 merge(ctas, (std::min(max_rows, e.rows) + kTreeMergeRows - 1) / kTreeMergeRows);
+  return cuda_status(
+      launch_after_previous(e.merge, merge, dim3(kTreeMergeRows * head_dim / 4), stream, p));
 }
 
 }  // namespace

@@ -70,23 +70,43 @@ struct TreeParams {
   // rows} (rows = 0: nothing to merge) and two pieces of ROWS rows.
   int4* ws_meta;
   float2* ws_ml;  // (max, sum) of each row of each piece
-  float* ws_o;    // [pieces][ROWS][D]
+  float* ws_o;    // [pieces][D / 4][ROWS][4]
 };
 
-constexpr int kTreeUnitCost = 1;
+// What a unit costs beside its tiles, in tiles.  Measured on B200 (us; 2 / 4 / 6 /
+// 9): GQA chat batch 86 / 71 / 69 / 70, its E4M3 form 107 / 98 / 89 / 88, the
+// LLaMA-7B batch 112 / 111 / 111 / 112.
+constexpr int kTreeUnitCost = 6;
 constexpr int kTreeMinTiles = 2;  // the shortest stretch worth a CTA
 constexpr int kTreeKeys = 64;     // keys per tile
 
-// The lengths of a sequence: false if it has nothing to do.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// The lengths of a sequence.
 struct TreeSeq {
   int ctx, q0, q_len;
 };
-__device__ __forceinline__ bool tree_seq(const TreeParams& p, int seq, TreeSeq& s, bool report) {
-  s.ctx = p.context_lens[seq];
-  s.q0 = p.query_start[seq];
-  const int end = p.query_start[seq + 1];
-  s.q_len = static_cast<int>(static_cast<unsigned>(end) - static_cast<unsigned>(s.q0));
-  if (s.ctx < 0 || s.ctx > p.max_context_len || end < s.q0 || s.q_len < 0 || s.q_len > s.ctx ||
+struct TreeLens {
+  int ctx, q0, end;
+};
+__device__ __forceinline__ TreeLens tree_lens(const TreeParams& p, int seq) {
+  return {p.context_lens[seq], p.query_start[seq], p.query_start[seq + 1]};
+}
+// False if the sequence has nothing to do.
+__device__ __forceinline__ bool tree_seq(const TreeParams& p, const TreeLens& x, TreeSeq& s,
+                                         bool report) {
+  s.ctx = x.ctx;
+  s.q0 = x.q0;
+  s.q_len = static_cast<int>(static_cast<unsigned>(x.end) - static_cast<unsigned>(x.q0));
+  if (s.ctx < 0 || s.ctx > p.max_context_len || x.end < s.q0 || s.q_len < 0 || s.q_len > s.ctx ||
       s.q_len > p.max_query_len || s.q0 < 0 || s.q0 > p.num_tokens - s.q_len) {
     if (report) set_err(p.err, PKV_DEVERR_BAD_CONTEXT);
     return false;
@@ -99,23 +119,26 @@ struct TreeItem {
   int seq, ctx, q0, q_len, kvh, rt, t0, t1, nt;
 };
 
-// Walks a CTA's stretch.  Every role walks on its own.
+// Walks a CTA's stretch.  Every role walks on its own.  The lengths of the
+// sequence after the one at hand are loaded ahead of their use.
 template <int ROWS>
 struct TreeWalk {
   int seq, unit, at;  // the next sequence, unit of it, and position in the unit
   int left;           // positions left in the stretch
   bool loaded;
   TreeSeq s;
+  TreeLens ahead;  // of sequence `seq`, until loaded; then of seq + 1
 
   __device__ __forceinline__ bool next(const TreeParams& p, TreeItem& it) {
     while (left > 0) {
       if (!loaded) {
         if (seq >= p.num_seqs) return false;
-        if (!tree_seq(p, seq, s, false)) {
+        loaded = tree_seq(p, ahead, s, false);
+        if (seq + 1 < p.num_seqs) ahead = tree_lens(p, seq + 1);
+        if (!loaded) {
           ++seq;
           continue;
         }
-        loaded = true;
       }
       const int nt = (s.ctx + kTreeKeys - 1) / kTreeKeys;
       const int rts = ((s.q_len << p.group_shift) + ROWS - 1) / ROWS;
@@ -125,7 +148,7 @@ struct TreeWalk {
       it.ctx = s.ctx;
       it.q0 = s.q0;
       it.q_len = s.q_len;
-      it.kvh = unit / rts;
+      it.kvh = rts == 1 ? unit : unit / rts;
       it.rt = unit - it.kvh * rts;
       it.t0 = max(0, at - kTreeUnitCost);
       it.t1 = max(0, at + take - kTreeUnitCost);
@@ -174,8 +197,8 @@ struct TreeTraits {
   static constexpr int OFF_KV = QT * Q_TILE;
   static constexpr int OFF_STG = OFF_KV + NS * STAGE;
   static constexpr int OFF_SEEN = OFF_STG + 2 * NSTG * STG_TILE;    // [ROWS][8] visible nodes
-  static constexpr int OFF_PAR = OFF_SEEN + ROWS * 32;              // [QT][256] parents
-  static constexpr int OFF_BAR = OFF_PAR + QT * PKV_MAX_TREE_NODES * 4;
+  static constexpr int OFF_PAR = OFF_SEEN + ROWS * 32;              // [QT][2][256] parents
+  static constexpr int OFF_BAR = OFF_PAR + QT * 2 * PKV_MAX_TREE_NODES * 4;
   static constexpr int B_KFULL = 0, B_KEMPTY = NS, B_VFULL = 2 * NS, B_VEMPTY = 3 * NS;
   static constexpr int B_STG = 4 * NS, B_STGEMPTY = B_STG + 2 * NSTG;
   static constexpr int B_Q = B_STGEMPTY + 2 * NSTG;  // per query tile: q, o_free, s[2], p[2], o[2]
@@ -258,7 +281,7 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
     const int last = min(p.num_seqs, first + per);
     auto weight = [&](int i, bool report) -> long long {
       TreeSeq s;
-      if (!tree_seq(p, i, s, report)) return 0;
+      if (!tree_seq(p, tree_lens(p, i), s, report)) return 0;
       const int rts = ((s.q_len << p.group_shift) + ROWS - 1) / ROWS;
       return static_cast<long long>(rts) * p.num_kv_heads *
              ((s.ctx + NKEY - 1) / NKEY + kTreeUnitCost);
@@ -308,6 +331,7 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
   walk.at = s_found[2];
   walk.left = s_found[3];
   walk.loaded = false;
+  walk.ahead = tree_lens(p, walk.seq);
   const int len = walk.left;
 
   if (warp == 1) {
@@ -349,19 +373,30 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
     const int shift = p.block_size == 16 ? 4 : 5;
     int gt = 0;
     bool ok = true;
-    while (ok && walk.next(p, it)) {
-      const int32_t* trow = p.block_tables + static_cast<size_t>(it.seq) * p.max_blocks_per_seq;
-      const int nblk = (it.ctx + p.block_size - 1) >> shift;
-      int chunk = -1, entry = -1;
+    // 32 entries of an item's table row at a time, an item's first ones while
+    // the item before it is under way
+    auto entries = [&](const TreeItem& x, int chunk) {
+      const int i = (chunk << 5) + lane;
+      return i < (x.ctx + p.block_size - 1) >> shift
+                 ? p.block_tables[static_cast<size_t>(x.seq) * p.max_blocks_per_seq + i]
+                 : -1;
+    };
+    auto first_chunk = [&](const TreeItem& x) { return (x.t0 * NKEY) >> (shift + 5); };
+    TreeItem nx;
+    bool more = walk.next(p, nx);
+    int ahead = more ? entries(nx, first_chunk(nx)) : -1;
+    while (ok && more) {
+      it = nx;
+      int chunk = first_chunk(it), entry = ahead;
+      more = walk.next(p, nx);
+      if (more) ahead = entries(nx, first_chunk(nx));
       for (int t = it.t0; t < it.t1; ++t, ++gt) {
         const int stage = gt % RING;
-        // this lane's 16 keys: the table is read 32 entries at a time
-        const int b0 = (t * NKEY) >> shift;
-        if ((b0 >> 5) != chunk) {
-          chunk = b0 >> 5;
-          const int i = (chunk << 5) + lane;
-          entry = i < nblk ? trow[i] : -1;
+        if (((t * NKEY) >> (shift + 5)) != chunk) {
+          chunk = (t * NKEY) >> (shift + 5);
+          entry = entries(it, chunk);
         }
+        // this lane's 16 keys
         const int piece = (lane / BOXES) % PIECES;
         const int key = t * NKEY + piece * 16;
         const int pb = __shfl_sync(kFullMask, entry, (key >> shift) & 31);
@@ -497,7 +532,7 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
     const int r = quarter * 32 + lane;
     const uint32_t tm = tmem + q * Tr::QCOLS + (static_cast<uint32_t>(quarter * 32) << 16);
     uint32_t* seen = reinterpret_cast<uint32_t*>(smem + Tr::OFF_SEEN) + (q * M + r) * 8;
-    int* par = reinterpret_cast<int*>(smem + Tr::OFF_PAR) + q * PKV_MAX_TREE_NODES;
+    int* par = reinterpret_cast<int*>(smem + Tr::OFF_PAR) + q * 2 * PKV_MAX_TREE_NODES;
     int met = 0;
     // a barrier of the query tile's softmax warps, bounded as every wait
     auto group_sync = [&] {
@@ -512,21 +547,37 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
       return static_cast<size_t>(x.q0 + (c >> p.group_shift)) * p.num_heads +
              (static_cast<size_t>(x.kvh) << p.group_shift) + (c & gmask);
     };
-    // the rows that exist go into shared memory (the others' S is not read)
-    auto load_q = [&](const TreeItem& x) {
+    // An item's query rows and its tree's parents come by cp.async, issued once
+    // the last S of the item before is complete; rows that do not exist are
+    // left as they are (nobody reads their S).
+    auto begin_load = [&](const TreeItem& x, int parity) {
       constexpr int CH = D / 8;
       const int n = rows_of(x, q) * CH;
-      unsigned char* qt = smem + q * Tr::Q_TILE;
-#pragma unroll 4
+      const uint32_t qt = sbase + q * Tr::Q_TILE;
       for (int i = r; i < n; i += 128) {
         const int row = i / CH, ch = i % CH;
-        uint4 u = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
-                                                  row_at(x, row) * D + ch * 8);
-        if constexpr (Tr::kQToFp16)
-          u = make_uint4(bf16x2_to_f16x2_sat(u.x), bf16x2_to_f16x2_sat(u.y),
-                         bf16x2_to_f16x2_sat(u.z), bf16x2_to_f16x2_sat(u.w));
-        *reinterpret_cast<uint4*>(qt + (ch >> 3) * Tr::Q_HALF + row * 128 +
-                                  (((ch & 7) ^ (row & 7)) << 4)) = u;
+        cp_async16(qt + (ch >> 3) * Tr::Q_HALF + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                   static_cast<const T*>(p.q) + row_at(x, row) * D + ch * 8);
+      }
+      if (partial(x, x.t1 - 1)) {
+        const int nodes = ((x.rt * ROWS + q * M + rows_of(x, q) - 1) >> p.group_shift) + 1;
+        for (int i = r; i < nodes; i += 128)
+          cp_async4(smem_addr(par + parity * PKV_MAX_TREE_NODES + i), p.parents + x.q0 + i);
+      }
+    };
+    auto end_load = [&](const TreeItem& x) {
+      cp_async_wait_all();
+      if constexpr (Tr::kQToFp16) {
+        constexpr int CH = D / 8;
+        const int n = rows_of(x, q) * CH;
+        for (int i = r; i < n; i += 128) {
+          const int row = i / CH, ch = i % CH;
+          uint4* at = reinterpret_cast<uint4*>(smem + q * Tr::Q_TILE + (ch >> 3) * Tr::Q_HALF +
+                                               row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+          const uint4 u = *at;
+          *at = make_uint4(bf16x2_to_f16x2_sat(u.x), bf16x2_to_f16x2_sat(u.y),
+                           bf16x2_to_f16x2_sat(u.z), bf16x2_to_f16x2_sat(u.w));
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -536,15 +587,22 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
     bool ok = true;
     TreeItem nx;
     bool more = walk.next(p, nx);
-    if (more && rows_of(nx, q) > 0) load_q(nx);
+    if (more && rows_of(nx, q) > 0) {
+      begin_load(nx, 1);
+      end_load(nx);
+    }
     while (ok && more) {
       it = nx;
       more = walk.next(p, nx);
       ++item;
+      const bool load_next = more && rows_of(nx, q) > 0;
       const int nrows = rows_of(it, q);
       if (nrows <= 0) {  // the second query tile of a unit of few rows
         gt += it.t1 - it.t0;
-        if (more && rows_of(nx, q) > 0) load_q(nx);
+        if (load_next) {
+          begin_load(nx, (item + 1) & 1);
+          end_load(nx);
+        }
         continue;
       }
       const bool active = r < nrows;
@@ -561,30 +619,26 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
       if (partial(it, it.t1 - 1)) {
         // the nodes that each row sees: itself, its parent, and so on
         const int node = (it.rt * ROWS + q * M + min(r, nrows - 1)) >> p.group_shift;
-        const int nodes = ((it.rt * ROWS + q * M + nrows - 1) >> p.group_shift) + 1;
-        ok = group_sync();  // nobody still follows the last item's parents
+        const int* up = par + (item & 1) * PKV_MAX_TREE_NODES;
+        ok = group_sync();  // every thread's share of the parents has arrived
         if (!ok) break;
-        for (int n = r; n < nodes; n += 128) {
-          int up = p.parents[it.q0 + n];
-          if (up < -1 || up >= n) {
-            set_err(p.err, PKV_DEVERR_BAD_TREE);
-            up = -1;
-          }
-          par[n] = up;
-        }
 #pragma unroll
         for (int w = 0; w < 8; ++w) seen[w] = 0;
-        ok = group_sync();
-        if (!ok) break;
         int at = node >> 5;
         uint32_t bits = 0;
-        for (int n = node; n >= 0; n = par[n]) {
+        for (int n = node; n >= 0;) {
           if ((n >> 5) != at) {
             seen[at] = bits;
             at = n >> 5;
             bits = 0;
           }
           bits |= 1u << (n & 31);
+          const int x = up[n];
+          if (x < -1 || x >= n) {
+            set_err(p.err, PKV_DEVERR_BAD_TREE);
+            break;
+          }
+          n = x;
         }
         seen[at] = bits;
       }
@@ -617,6 +671,8 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
           break;
         }
         tc::tc_fence_after();
+        // every S of this item is complete: its query tile may be replaced
+        if (t == it.t1 - 1 && load_next) begin_load(nx, (item + 1) & 1);
         const bool cut = partial(it, t);
         if (warp_active) {
           const uint32_t sbuf = tm + b * NKEY;
@@ -749,8 +805,7 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
         if (lane == 0) mbar_arrive(bar_p(q, b));
       }
       if (!ok) break;
-      // every S of this item is complete, so its query tile may be replaced
-      if (more && rows_of(nx, q) > 0) load_q(nx);
+      if (load_next) end_load(nx);
       // ---- output ------------------------------------------------------------------
       ok = mbar_wait_bounded(bar_o(q, (tq - 1) & 1), ((tq - 1) >> 1) & 1);
       if (!__all_sync(kFullMask, ok)) {
@@ -806,10 +861,11 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
             *reinterpret_cast<uint4*>(o) = pack8(a, typename Tr::DT());
             *reinterpret_cast<uint4*>(o + 8) = pack8(z, typename Tr::DT());
           } else {
-            float4* o = reinterpret_cast<float4*>(p.ws_o + slot * D + c);
+            // [D / 4][ROWS] of 4 floats: a warp's rows side by side
+            float4* o = reinterpret_cast<float4*>(p.ws_o) + (slot - q * M - r) * (D / 4) + q * M + r;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              o[i] = make_float4(v[4 * i] * v_scale, v[4 * i + 1] * v_scale,
+              o[(c / 4 + i) * ROWS] = make_float4(v[4 * i] * v_scale, v[4 * i + 1] * v_scale,
                                  v[4 * i + 2] * v_scale, v[4 * i + 3] * v_scale);
           }
         }
@@ -906,53 +962,46 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
 // Joins the pieces of the units that lie across CTAs' stretches: with M = max m,
 //   out = sum 2^(m - M) o / sum 2^(m - M) l.
 // Entry blockIdx.x is of the unit that ended in that CTA; the piece of the unit's
-// first CTA is that CTA's second, of every later one its first.  A warp per row;
-// blockIdx.y takes 8 rows.
+// first CTA is that CTA's second, of every later one its first.  A thread has 4
+// dims of a row, a warp 2 rows x 64 dims (whole sectors of the pieces);
+// blockIdx.y takes kTreeMergeRows rows.
+constexpr int kTreeMergeRows = 8;
 template <int D, int ROWS, class DT>
-__global__ void __launch_bounds__(256) paged_attn_tree_merge_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(kTreeMergeRows * D / 4)
+    paged_attn_tree_merge_kernel(const TreeParams p) {
   using T = typename DT::T;
-  constexpr int N = D / 32;
   grid_dependency_wait();
   trigger_dependents();
   const int4 e = p.ws_meta[blockIdx.x];
-  const int r = static_cast<int>(blockIdx.y) * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = static_cast<int>(blockIdx.y) * kTreeMergeRows + (w / (D / 64)) * 2 + (lane & 1);
+  const int c4 = (w % (D / 64)) * 16 + (lane >> 1);
   if (r >= e.w) return;
   const int last = static_cast<int>(blockIdx.x);
-  auto slot = [&](int c) {
-    return (static_cast<size_t>(c) * 2 + (c == e.z ? 1 : 0)) * ROWS + r;
-  };
-  float big = -INFINITY;
-  for (int c = e.z + lane; c <= last; c += 32) big = fmaxf(big, p.ws_ml[slot(c)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(kFullMask, big, o));
-  float num[N] = {}, den = 0.f;
+  auto piece = [&](int c) { return static_cast<size_t>(c) * 2 + (c == e.z ? 1 : 0); };
+  // an online sum, so that every load of a piece is under way at once
+  float big = -INFINITY, num[4] = {}, den = 0.f;
 #pragma unroll 4
   for (int c = e.z; c <= last; ++c) {
-    const float2 ml = p.ws_ml[slot(c)];
-    const float f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - big);
-    float o[N];
-    if constexpr (N == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p.ws_o + slot(c) * D + lane * N);
-      o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(p.ws_o + slot(c) * D + lane * N);
-      o[0] = v.x, o[1] = v.y;
-    }
-    den = fmaf(f, ml.y, den);
-#pragma unroll
-    for (int i = 0; i < N; ++i) num[i] = fmaf(f, o[i], num[i]);
+    const float2 ml = p.ws_ml[piece(c) * ROWS + r];
+    const float4 o = reinterpret_cast<const float4*>(p.ws_o)[(piece(c) * (D / 4) + c4) * ROWS + r];
+    const float m = ml.x == -INFINITY ? big : fmaxf(big, ml.x);
+    const float a = big == -INFINITY ? 0.f : exp2_approx(big - m);
+    const float f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - m);
+    big = m;
+    den = den * a + f * ml.y;
+    num[0] = num[0] * a + f * o.x;
+    num[1] = num[1] * a + f * o.y;
+    num[2] = num[2] * a + f * o.z;
+    num[3] = num[3] * a + f * o.w;
   }
   const float inv = den > 0.f || den != den ? 1.f / den : 0.f;
   T* out = static_cast<T*>(p.out) +
            (static_cast<size_t>(e.x + (r >> p.group_shift)) * p.num_heads +
             (static_cast<size_t>(e.y) << p.group_shift) + (r & ((1 << p.group_shift) - 1))) * D +
-           lane * N;
-  if constexpr (N == 4)
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack2(num[0] * inv, num[1] * inv, DT()),
-                                                pack2(num[2] * inv, num[3] * inv, DT()));
-  else
-    *reinterpret_cast<uint32_t*>(out) = pack2(num[0] * inv, num[1] * inv, DT());
+           c4 * 4;
+  *reinterpret_cast<uint2*>(out) = make_uint2(pack2(num[0] * inv, num[1] * inv, DT()),
+                                              pack2(num[2] * inv, num[3] * inv, DT()));
 }
 
 }  // namespace pkv
