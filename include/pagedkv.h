@@ -682,7 +682,7 @@ pkv_status pkv_paged_attn_tree_fp8(void* out, const void* q, const void* k_cache
  *   accept_uniforms  device float [T] in [0, 1); a root's is not read
  *   sample_uniforms  device float [num_seqs] in [0, 1)
  * All pointers are aligned to their elements' size; the rows may start at any
- * element.  A sequence whose q_len is negative or above max_query_len, or
+ * element.  vocab_size is at most 2^30 (above: PKV_ERR_UNSUPPORTED).  A sequence whose q_len is negative or above max_query_len, or
  * whose rows leave [0, num_tokens), sets PKV_DEVERR_BAD_CONTEXT and is treated
  * as one without nodes.  A drafted token outside [0, vocab_size) that is tried
  * sets PKV_DEVERR_BAD_DRAFT and is passed over (r and Z stay); weights whose

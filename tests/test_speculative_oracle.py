@@ -307,6 +307,7 @@ def test_verify_refusals(pk):
                  dict(q=ctypes.c_void_p(0x1002)), dict(dt=0, p=ctypes.c_void_p(0x1001))):
         assert verify_call(pk, **over) == inv, over
     assert verify_call(pk, mq=257) == uns
+    assert verify_call(pk, vocab=2 ** 30 + 1, ps=2 ** 31, qstr=2 ** 31) == uns
     assert verify_call(pk, num_seqs=0) == pk.OK
 
 
