@@ -2,10 +2,17 @@
 // model accepts, and the token that follows them.
 //
 // Per sequence: a walk down the tree from gathered probabilities, and for each
-// residual r = max(r / Z - q, 0) that a rejection leaves, and for the last
-// distribution, one pass over a row of the target (and of the draft): its sum
-// and then the first x whose running sum passes the drawn share.  What bounds it
-// is reading those rows, vocab_size values each.
+// residual that a rejection leaves, and for the last distribution, one pass over
+// a row of the target (and of the draft): its sum, and then the first x whose
+// running sum passes the drawn share.  What bounds it is reading those rows,
+// vocab_size values each.
+//
+// The residual after k rejections, r_k = max(r_(k-1) / Z_(k-1) - q, 0) with
+// Z_k = sum r_k, Z_0 = 1, needs no division and no memory of the steps: with
+// c_k = Z_0 ... Z_(k-1), r_k c_k = max(p - (c_1 + ... + c_k) q, 0), as clipping at 0
+// between subtractions changes nothing.  So with S_0 = 1 and A_0 = 0
+//   A_k = A_(k-1) + S_(k-1),  s_k = max(p - A_k q, 0),  S_k = sum s_k  (= c_(k+1)),
+// the next token is drawn from s_k, and u q Z_k < r_k is u q S_k < s_k.
 //
 // A cluster of 1 to 8 CTAs serves a sequence.  Rank 0 gathers what the walk
 // needs (each node's parent, token, uniform, and the two probabilities of its
@@ -17,7 +24,7 @@
 #include <cooperative_groups.h>
 #include <math.h>
 
-#include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "host_common.h"
@@ -76,19 +83,16 @@ struct VerifyShared {
   int parent[PKV_MAX_TREE_NODES], token[PKV_MAX_TREE_NODES];
   float u[PKV_MAX_TREE_NODES];
   float p[PKV_MAX_TREE_NODES], q[PKV_MAX_TREE_NODES];  // of the node's token, at its parent
-  double z[PKV_MAX_TREE_NODES + 1];    // Z before each rejection at the current node
+  double taken;                        // A of the rejections at the current node
   int rejected[PKV_MAX_TREE_NODES];    // the tokens rejected there
   double warp_sum[kVerifyWarps];
   double cta_sum[2][kMaxCluster];      // by parity of the pass
   int cur, nrej, more;
 };
 
-// What is left of weight p after nrej rejections of draws from q.
-__device__ __forceinline__ double residual(double p, float q, const double* z, int nrej) {
-  double r = p;
-  for (int k = 0; k < nrej && r > 0.0; ++k)
-    r = fmax((k == 0 ? r : r / z[k]) - static_cast<double>(q), 0.0);  // z[0] = 1
-  return r;
+// What is left of weight p of a token that the draft weighs q: max(p - A q, 0).
+__device__ __forceinline__ double residual(float p, float q, double taken) {
+  return fmax(fma(-taken, static_cast<double>(q), static_cast<double>(p)), 0.0);
 }
 
 template <class T>
@@ -151,65 +155,128 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
     return;
   }
 
-  // This warp's piece of a row of node `cur`: 32 groups at a time, in the order of
-  // the vocabulary.  f(x0, r) sees a lane's group and its residual weights, and
-  // says whether to go on.
+  // This warp's piece of the row of node `cur`: chunks c0 .. c1 - 1 of 32 groups, in
+  // the order of the vocabulary; f0 .. f1 - 1 of them lie wholly within the row.
   const int gw = rank * kVerifyWarps + warp;
-  auto scan = [&](int cur, int nrej, auto&& f) {
-    const T* prow = target + (q0 + cur) * p.target_stride;
-    const T* qrow = certain ? nullptr : draft + (q0 + cur) * p.draft_stride;
-    const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(prow) / sizeof(T)) % V);
-    const bool same =
-        !certain && (reinterpret_cast<uintptr_t>(qrow) / sizeof(T)) % V == shift;
-    const int groups = static_cast<int>((static_cast<unsigned>(p.vocab) + shift + V - 1) / V);
-    const int chunks = (groups + 31) / 32;
+  struct Piece {
+    const T *p, *q;
+    int shift, c0, c1, f0, f1;
+    bool same;                              // q's groups are aligned as p's
+    unsigned hit[PKV_MAX_TREE_NODES / 32];  // certain draft: which rejected tokens lie in it
+    unsigned hits;
+  };
+  auto piece_of = [&](int cur, int nrej) {
+    Piece x;
+    x.p = target + (q0 + cur) * p.target_stride;
+    x.q = certain ? nullptr : draft + (q0 + cur) * p.draft_stride;
+    x.shift = static_cast<int>((reinterpret_cast<uintptr_t>(x.p) / sizeof(T)) % V);
+    x.same = certain || nrej == 0 ||
+             static_cast<int>((reinterpret_cast<uintptr_t>(x.q) / sizeof(T)) % V) == x.shift;
+    const int chunks = (p.vocab + x.shift + 32 * V - 1) / (32 * V);
     const int per = (chunks + ranks * kVerifyWarps - 1) / (ranks * kVerifyWarps);
-    const int c0 = min(chunks, gw * per), c1 = min(chunks, c0 + per);
-    const int lo = c0 * 32 * V - shift, hi = c1 * 32 * V - shift;  // this warp's values
-    // certain draft: which of the first 32 x 8 rejected tokens lie in this piece
-    unsigned hit[PKV_MAX_TREE_NODES / 32] = {};
-    if (certain) {
+    x.c0 = min(chunks, gw * per);
+    x.c1 = min(chunks, x.c0 + per);
+    x.f0 = max(x.c0, x.shift > 0 ? 1 : 0);
+    x.f1 = x.same ? min(x.c1, (p.vocab + x.shift) / (32 * V)) : x.f0;
+    const int lo = x.c0 * 32 * V - x.shift, hi = x.c1 * 32 * V - x.shift;
+    x.hits = 0;
 #pragma unroll
-      for (int b = 0; b < PKV_MAX_TREE_NODES / 32; ++b) {
-        if (b * 32 >= nrej) break;
-        const int x = b * 32 + lane < nrej ? sh.rejected[b * 32 + lane] : -1;
-        hit[b] = __ballot_sync(kFullMask, x >= 0 && x >= lo && x < hi);
+    for (int b = 0; b < PKV_MAX_TREE_NODES / 32; ++b) {
+      x.hit[b] = 0;
+      if (certain && b * 32 < nrej) {
+        const int t = b * 32 + lane < nrej ? sh.rejected[b * 32 + lane] : -1;
+        x.hit[b] = __ballot_sync(kFullMask, t >= 0 && t >= lo && t < hi);
+        x.hits |= x.hit[b];
       }
     }
-    const bool with_q = !certain && nrej > 0;
-#pragma unroll 2
-    for (int c = c0; c < c1; ++c) {
-      const int x0 = (c * 32 + lane) * V - shift;
-      float pf[V], qf[V] = {};
-      load_group<T>(prow, true, x0, p.vocab, pf);
-      if (with_q) load_group<T>(qrow, same, x0, p.vocab, qf);
-      double r[V];
+    return x;
+  };
+  // A lane's residual weights of chunk c, any chunk.
+  auto chunk_weights = [&](const Piece& x, int c, double taken, double (&r)[V]) {
+    const int x0 = (c * 32 + lane) * V - x.shift;
+    float pf[V], qf[V] = {};
+    load_group<T>(x.p, true, x0, p.vocab, pf);
+    if (taken > 0.0) load_group<T>(x.q, x.same, x0, p.vocab, qf);
 #pragma unroll
-      for (int e = 0; e < V; ++e)
-        r[e] = with_q ? residual(pf[e], qf[e], sh.z, nrej) : static_cast<double>(pf[e]);
-      if (certain) {
+    for (int e = 0; e < V; ++e) r[e] = residual(pf[e], qf[e], taken);
+    if (x.hits != 0) {
 #pragma unroll
-        for (int b = 0; b < PKV_MAX_TREE_NODES / 32; ++b)
-          for (unsigned m = hit[b]; m != 0; m &= m - 1) {
-            const int x = sh.rejected[b * 32 + __ffs(m) - 1];
+      for (int b = 0; b < PKV_MAX_TREE_NODES / 32; ++b)
+        for (unsigned m = x.hit[b]; m != 0; m &= m - 1) {
+          const int t = sh.rejected[b * 32 + __ffs(m) - 1];
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-              if (x0 + e == x) r[e] = 0.0;
-          }
-      }
-      if (!f(x0, r)) break;
+          for (int e = 0; e < V; ++e)
+            if (x0 + e == t) r[e] = 0.0;
+        }
     }
+    return x0;
   };
   int passes = 0;
   // The sum of node cur's residual weights, the same in every thread of the
   // cluster; sh.warp_sum and sh.cta_sum[...] hold its parts.
-  auto pass = [&](int cur, int nrej) {
+  auto pass = [&](int cur, int nrej, double taken) {
+    const Piece x = piece_of(cur, nrej);
     double s = 0.0;
-    scan(cur, nrej, [&](int, const double (&r)[V]) {
+    int c = x.c0;
+    if (x.hits == 0) {
+      auto edge = [&](int to) {
+        for (; c < to; ++c) {
+          double r[V];
+          chunk_weights(x, c, taken, r);
 #pragma unroll
-      for (int e = 0; e < V; ++e) s += r[e];
-      return true;
-    });
+          for (int e = 0; e < V; ++e) s += r[e];
+        }
+      };
+      edge(min(x.f0, x.c1));
+      // whole chunks, kBatch loads of each row under way at once
+      constexpr int kBatch = 16 / V;
+      auto whole = [&](auto with_q, auto add) {
+        for (; c < x.f1; c += kBatch) {
+          uint4 pu[kBatch], qu[kBatch];
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            pu[b] = qu[b] = make_uint4(0u, 0u, 0u, 0u);
+            if (c + b < x.f1) {
+              const int64_t at = static_cast<int64_t>((c + b) * 32 + lane) * V - x.shift;
+              pu[b] = __ldg(reinterpret_cast<const uint4*>(x.p + at));
+              if constexpr (decltype(with_q)::value) qu[b] = __ldg(reinterpret_cast<const uint4*>(x.q + at));
+            }
+          }
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const T* pt = reinterpret_cast<const T*>(&pu[b]);
+            const T* qt = reinterpret_cast<const T*>(&qu[b]);
+#pragma unroll
+            for (int e = 0; e < V; ++e) add(weight_of(pt[e]), weight_of(qt[e]));
+          }
+        }
+        c = x.f1;
+      };
+      if (c < x.f1) {
+        if (taken == 0.0) {
+          whole(std::false_type(), [&](float a, float) { s += static_cast<double>(a); });
+        } else if (taken == 1.0) {
+          // a - b for a > b as a float and its exact error: one conversion
+          float low = 0.f;
+          whole(std::true_type(), [&](float a, float b) {
+            const float d = fmaxf(a - b, 0.f);
+            s += static_cast<double>(d);
+            if (d > 0.f && d < INFINITY) low += (a - d) - b;
+          });
+          s += static_cast<double>(low);
+        } else {
+          whole(std::true_type(), [&](float a, float b) { s += residual(a, b, taken); });
+        }
+      }
+      edge(x.c1);
+    } else {
+      for (; c < x.c1; ++c) {
+        double r[V];
+        chunk_weights(x, c, taken, r);
+#pragma unroll
+        for (int e = 0; e < V; ++e) s += r[e];
+      }
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
     if (lane == 0) sh.warp_sum[warp] = s;
@@ -222,16 +289,14 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
     }
     cluster.sync();
     double t = 0.0;
-    for (int c = 0; c < ranks; ++c) t += sh.cta_sum[par][c];
+    for (int k = 0; k < ranks; ++k) t += sh.cta_sum[par][k];
     return t;
   };
 
   // ---- the walk: warp 0 of every CTA, until it needs a residual's sum ---------------
   int cur = 0, nrej = 0, next = 1, count = 1;
-  if (tid == 0) {
-    sh.z[0] = 1.0;
-    if (rank == 0) acc[0] = 0;
-  }
+  double taken = 0.0, left = 1.0;  // A and S (a certain draft: A stays 0)
+  if (rank == 0 && tid == 0) acc[0] = 0;
   double total = 0.0;
   bool summed = false;  // total is that of (cur, nrej)
   for (;;) {
@@ -252,40 +317,40 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
           if (rank == 0 && lane == 0) set_err(p.err, PKV_DEVERR_BAD_DRAFT);
           continue;
         }
-        double r = sh.p[j];
+        double r, q = 1.0;
         if (certain) {
           bool before = false;
           for (int k = lane; k < nrej; k += 32) before |= sh.rejected[k] == x;
-          if (__any_sync(kFullMask, before)) r = 0.0;
+          r = __any_sync(kFullMask, before) ? 0.0 : static_cast<double>(sh.p[j]);
         } else {
-          r = residual(r, sh.q[j], sh.z, nrej);
+          q = static_cast<double>(sh.q[j]);
+          r = residual(sh.p[j], sh.q[j], taken);
         }
-        const double q = certain ? 1.0 : static_cast<double>(sh.q[j]);
-        if (static_cast<double>(sh.u[j]) * q * sh.z[nrej] < r) {
+        summed = false;
+        if (static_cast<double>(sh.u[j]) * q * left < r) {
           cur = j;
           nrej = 0;
+          taken = 0.0;
+          left = 1.0;
           if (rank == 0 && lane == 0) acc[count] = j;
           ++count;
-          summed = false;
-        } else {
-          const double left = sh.z[nrej] - r;
+        } else if (certain) {
           __syncwarp();
-          if (lane == 0) {
-            sh.rejected[nrej] = x;
-            if (certain) sh.z[nrej + 1] = left;
-          }
+          if (lane == 0) sh.rejected[nrej] = x;
           __syncwarp();
           ++nrej;
-          summed = false;
-          if (!certain) {
-            more = true;
-            break;
-          }
+          left -= r;
+        } else {
+          ++nrej;
+          taken += left;
+          more = true;
+          break;
         }
       }
       if (lane == 0) {
         sh.cur = cur;
         sh.nrej = nrej;
+        sh.taken = taken;
         // 1: sum and walk on; 0: the end, with the last sum still good; 2: the end
         sh.more = more ? 1 : summed ? 0 : 2;
       }
@@ -294,14 +359,16 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
     const int what = sh.more;
     cur = sh.cur;
     nrej = sh.nrej;
-    if (what != 0) total = pass(cur, nrej);
+    taken = sh.taken;
+    if (what != 0) total = pass(cur, nrej, taken);
     if (what != 1) break;
     summed = true;
-    if (tid == 0) sh.z[nrej] = total;
+    left = total;
   }
   if (!(total > 0.0) && nrej > 0) {  // nothing left: the target's own weights again
     nrej = 0;
-    total = pass(cur, 0);
+    taken = 0.0;
+    total = pass(cur, 0, 0.0);
   }
   // ---- the next token ------------------------------------------------------------------
   if (rank == 0) {
@@ -342,8 +409,12 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
   }
   if (owner < 0) owner = last, base = fallback;
   if (warp != owner) return;
+  const Piece x = piece_of(cur, nrej);
   int found = -1, positive = -1;
-  scan(cur, nrej, [&](int x0, const double (&r)[V]) {
+#pragma unroll 2
+  for (int c = x.c0; c < x.c1; ++c) {
+    double r[V];
+    const int x0 = chunk_weights(x, c, taken, r);
     double s = 0.0;
     int pos = -1;
 #pragma unroll
@@ -357,23 +428,24 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
       const double y = __shfl_up_sync(kFullMask, upto, o);
       if (lane >= o) upto += y;
     }
-    double c = base + (upto - s);
-    int mine = -1;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      c += r[e];
-      if (mine < 0 && r[e] > 0.0 && c > want) mine = x0 + e;
-    }
-    const unsigned m = __ballot_sync(kFullMask, mine >= 0);
     const unsigned any = __ballot_sync(kFullMask, pos >= 0);
     if (any != 0) positive = __shfl_sync(kFullMask, pos, 31 - __clz(any));
-    if (m != 0) {
-      found = __shfl_sync(kFullMask, mine, __ffs(m) - 1);
-      return false;
+    if (__any_sync(kFullMask, base + upto > want)) {
+      double sum = base + (upto - s);
+      int mine = -1;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        sum += r[e];
+        if (mine < 0 && r[e] > 0.0 && sum > want) mine = x0 + e;
+      }
+      const unsigned m = __ballot_sync(kFullMask, mine >= 0);
+      if (m != 0) {
+        found = __shfl_sync(kFullMask, mine, __ffs(m) - 1);
+        break;
+      }
     }
     base += __shfl_sync(kFullMask, upto, 31);
-    return true;
-  });
+  }
   if (lane == 0) p.next_token[seq] = found >= 0 ? found : positive;
 }
 
