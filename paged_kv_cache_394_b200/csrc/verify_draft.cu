@@ -155,9 +155,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
     return;
   }
 
-  // This warp's piece of the row of node `cur`: chunks c0 .. c1 - 1 of 32 groups, in
+  // Warp gw's piece of the row of node `cur`: chunks c0 .. c1 - 1 of 32 groups, in
   // the order of the vocabulary; f0 .. f1 - 1 of them lie wholly within the row.
-  const int gw = rank * kVerifyWarps + warp;
   struct Piece {
     const T *p, *q;
     int shift, c0, c1, f0, f1;
@@ -165,7 +164,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
     unsigned hit[PKV_MAX_TREE_NODES / 32];  // certain draft: which rejected tokens lie in it
     unsigned hits;
   };
-  auto piece_of = [&](int cur, int nrej) {
+  auto piece_of = [&](int cur, int nrej, int gw) {
     Piece x;
     x.p = target + (q0 + cur) * p.target_stride;
     x.q = certain ? nullptr : draft + (q0 + cur) * p.draft_stride;
@@ -215,7 +214,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
   // The sum of node cur's residual weights, the same in every thread of the
   // cluster; sh.warp_sum and sh.cta_sum[...] hold its parts.
   auto pass = [&](int cur, int nrej, double taken) {
-    const Piece x = piece_of(cur, nrej);
+    const Piece x = piece_of(cur, nrej, rank * kVerifyWarps + warp);
     double s = 0.0;
     int c = x.c0;
     if (x.hits == 0) {
@@ -408,10 +407,35 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
     at += sh.warp_sum[w];
   }
   if (owner < 0) owner = last, base = fallback;
+  // all warps of the CTA sum a part of that warp's piece; the part that passes
+  // the share is scanned
+  Piece x = piece_of(cur, nrej, rank * kVerifyWarps + owner);
+  const int share = (x.c1 - x.c0 + kVerifyWarps - 1) / kVerifyWarps;
+  const int first = min(x.c1, x.c0 + warp * share);
+  x.c1 = min(x.c1, first + share);
+  x.c0 = first;
+  double part = 0.0;
+  for (int c = x.c0; c < x.c1; ++c) {
+    double r[V];
+    chunk_weights(x, c, taken, r);
+#pragma unroll
+    for (int e = 0; e < V; ++e) part += r[e];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(kFullMask, part, o);
+  __syncthreads();  // everyone has chosen by the sums of the pass
+  if (lane == 0) sh.warp_sum[warp] = part;
+  __syncthreads();
+  at = base;
+  owner = -1;
+  for (int w = 0; w < kVerifyWarps && owner < 0; ++w) {
+    if (sh.warp_sum[w] > 0.0) last = w, fallback = at;
+    if (at + sh.warp_sum[w] > want) owner = w, base = at;
+    at += sh.warp_sum[w];
+  }
+  if (owner < 0) owner = last, base = fallback;
   if (warp != owner) return;
-  const Piece x = piece_of(cur, nrej);
   int found = -1, positive = -1;
-#pragma unroll 2
   for (int c = x.c0; c < x.c1; ++c) {
     double r[V];
     const int x0 = chunk_weights(x, c, taken, r);
