@@ -8,6 +8,7 @@ through the C ABI.  Importing this module loads the library and raises
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -175,12 +176,13 @@ def _cache_dtype_code(t):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _dev(t, name, dtype=None):
@@ -660,8 +662,119 @@ def _same_device(*tensors):
     """All tensors (Nones left out) on the calling thread's current device."""
     here = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.device.index != here:
+        if t is not None and t.get_device() != here:
             raise ValueError("all tensors must be on the current CUDA device (%d)" % here)
+
+
+def _devs(names, tensors, dtype=None):
+    """Every tensor contiguous, of the dtype if given, and on the current device."""
+    here = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    for t in tensors:
+        if (t.get_device() != here or not t.is_contiguous()
+                or (dtype is not None and t.dtype != dtype)):
+            break
+    else:
+        return
+    for n, t in zip(names, tensors):
+        _dev(t, n, dtype)
+    _same_device(*tensors)
+
+
+def _tree_args(out, q, k_cache, v_cache, block_tables, context_lens, query_start, parents,
+               num_kv_heads, block_size, dev_err):
+    _devs(("out", "q", "k_cache", "v_cache"), (out, q, k_cache, v_cache))
+    _devs(("block_tables", "context_lens", "query_start", "parents"),
+          (block_tables, context_lens, query_start, parents), torch.int32)
+    _same_device(dev_err)
+    t, h, d = q.shape
+    num_blocks, hkv, bs, dk = k_cache.shape
+    s = context_lens.shape[0]
+    if (hkv, bs, dk) != (num_kv_heads, block_size, d) or out.shape != q.shape:
+        raise ValueError("shape mismatch")
+    if query_start.shape != (s + 1,) or block_tables.shape[0] != s:
+        raise ValueError("query_start must be [S+1], block_tables [S, max_blocks]")
+    if q.dtype != k_cache.dtype or out.dtype != q.dtype:
+        raise TypeError("q, out and caches must share a dtype")
+    if plan is not None:
+        pa, (ws_ptr, ws_bytes, _ws) = _plan_args(plan, workspace, q.device, stream)
+        _check(_paged_attn_prefill_planned(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                           _ptr(block_tables), _ptr(context_lens),
+                                           _ptr(query_start), *pa, float(scale), s, t, h, hkv, d,
+                                           bs, block_tables.shape[1], max_context_len,
+                                           max_query_len, num_blocks, _dtype_code(q), ws_ptr,
+                                           ws_bytes, _ptr(dev_err), _stream(stream)),
+               "paged_attn_prefill_planned")
+        return
+    _check(_paged_attn_prefill(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                               _ptr(block_tables), _ptr(context_lens), _ptr(query_start),
+                               float(scale), s, t, h, hkv, d, bs, block_tables.shape[1],
+                               max_context_len, max_query_len, num_blocks, _dtype_code(q),
+                               _ptr(dev_err), _stream(stream)),
+           "paged_attn_prefill")
+
+
+def paged_attn_prefill_fp8(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
+                           scale, k_scales, v_scales, num_kv_heads, block_size, max_context_len,
+                           max_query_len, dev_err=None, stream=None, plan=None, workspace=None):
+    """Chunked-prefill attention over E4M3 caches (values = code * scale of the
+    kv head); q and out are 16-bit.  ``plan`` and ``workspace`` as for
+    paged_attn_prefill.  See include/pagedkv.h."""
+    for n, t in (("out", out), ("q", q), ("k_cache", k_cache), ("v_cache", v_cache)):
+        _dev(t, n)
+    _dev(block_tables, "block_tables", torch.int32)
+    _dev(context_lens, "context_lens", torch.int32)
+    _dev(query_start, "query_start", torch.int32)
+    t, h, d = q.shape
+    num_blocks, hkv, bs, dk = k_cache.shape
+    s = context_lens.shape[0]
+    if (hkv, bs, dk) != (num_kv_heads, block_size, d) or out.shape != q.shape:
+        raise ValueError("shape mismatch")
+    if query_start.shape != (s + 1,) or block_tables.shape[0] != s:
+        raise ValueError("query_start must be [S+1], block_tables [S, max_blocks]")
+    if _cache_dtype_code(k_cache) != FP8_E4M3 or v_cache.dtype != k_cache.dtype:
+        raise TypeError("E4M3 caches must be uint8 (or float8_e4m3fn)")
+    if out.dtype != q.dtype:
+        raise TypeError("q and out must share a dtype")
+    ks, vs = _scales_for(k_scales, v_scales, hkv, q.device, stream)
+    if plan is not None:
+        pa, (ws_ptr, ws_bytes, _ws) = _plan_args(plan, workspace, q.device, stream)
+        _check(_paged_attn_prefill_fp8_planned(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                               _ptr(block_tables), _ptr(context_lens),
+                                               _ptr(query_start), *pa, float(scale), _ptr(ks),
+                                               _ptr(vs), s, t, h, hkv, d, bs,
+                                               block_tables.shape[1], max_context_len,
+                                               max_query_len, num_blocks, _dtype_code(q), ws_ptr,
+                                               ws_bytes, _ptr(dev_err), _stream(stream)),
+               "paged_attn_prefill_fp8_planned")
+        return
+    _check(_paged_attn_prefill_fp8(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                   _ptr(block_tables), _ptr(context_lens), _ptr(query_start),
+                                   float(scale), _ptr(ks), _ptr(vs), s, t, h, hkv, d, bs,
+                                   block_tables.shape[1], max_context_len, max_query_len,
+                                   num_blocks, _dtype_code(q), _ptr(dev_err), _stream(stream)),
+           "paged_attn_prefill_fp8")
+
+
+def _same_device(*tensors):
+    """All tensors (Nones left out) on the calling thread's current device."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError("all tensors must be on the current CUDA device (%d)" % here)
+
+
+def _devs(names, tensors, dtype=None):
+    """Every tensor contiguous, of the dtype if given, and on the current device."""
+    here = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    for t in tensors:
+        if (t.get_device() != here or not t.is_contiguous()
+                or (dtype is not None and t.dtype != dtype)):
+            break
+    else:
+        return
+    for n, t in zip(names, tensors):
+        _dev(t, n, dtype)
+    _same_device(*tensors)
 
 
 def _tree_args(out, q, k_cache, v_cache, block_tables, context_lens, query_start, parents,
@@ -687,6 +800,7 @@ def _tree_args(out, q, k_cache, v_cache, block_tables, context_lens, query_start
     return s, t, h, d, num_blocks
 
 
+@functools.lru_cache(maxsize=256)
 def tree_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len,
                          max_query_len):
     """Scratch bytes paged_attn_tree and paged_attn_tree_fp8 need for this shape."""
@@ -697,13 +811,13 @@ def tree_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, max_contex
 def _tree_workspace(workspace, s, h, hkv, d, max_context_len, max_query_len, device, stream):
     """(the workspace, its bytes); allocated if None."""
     if workspace is None:
-        need = _tree_workspace_bytes(s, h, hkv, d, max_context_len, max_query_len)
+        need = tree_workspace_bytes(s, h, hkv, d, max_context_len, max_query_len)
         if not need:
             return None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if stream is not None:
-            workspace.record_stream(stream)   # the temporary must outlive the launch
-        return workspace, need
+        if stream is None:
+            return torch.empty(need, dtype=torch.uint8, device=device), need
+        with torch.cuda.stream(stream):   # memory of the stream that writes it
+            return torch.empty(need, dtype=torch.uint8, device=device), need
     _dev(workspace, "workspace")
     _same_device(workspace)
     return workspace, workspace.numel() * workspace.element_size()
@@ -780,14 +894,11 @@ def verify_draft(accepted, num_accepted, next_token, target_probs, draft_tokens,
     the token that follows into next_token [S].  draft_probs [T, V] are the
     distributions the children were drawn from; None takes the draft as
     certain of its tokens.  See include/pagedkv.h."""
-    for n, t in (("accepted", accepted), ("num_accepted", num_accepted),
-                 ("next_token", next_token), ("draft_tokens", draft_tokens),
-                 ("parents", parents), ("query_start", query_start)):
-        _dev(t, n, torch.int32)
-    _dev(accept_uniforms, "accept_uniforms", torch.float32)
-    _dev(sample_uniforms, "sample_uniforms", torch.float32)
-    _same_device(accepted, num_accepted, next_token, target_probs, draft_tokens, parents,
-                 query_start, accept_uniforms, sample_uniforms, draft_probs, dev_err)
+    _devs(("accepted", "num_accepted", "next_token", "draft_tokens", "parents", "query_start"),
+          (accepted, num_accepted, next_token, draft_tokens, parents, query_start), torch.int32)
+    _devs(("accept_uniforms", "sample_uniforms"), (accept_uniforms, sample_uniforms),
+          torch.float32)
+    _same_device(target_probs, draft_probs, dev_err)
     if target_probs.dim() != 2:
         raise ValueError("target_probs must be [T, vocab]")
     t, v = target_probs.shape
@@ -814,14 +925,10 @@ def compact_accepted(k_cache, v_cache, block_tables, context_lens, query_start, 
     """Move the K/V of each tree's kept nodes (accepted [S, max_query_len] and
     num_accepted [S], as verify_draft writes them) to the front of the tree's
     cache positions, in place.  16-bit or E4M3 caches.  See include/pagedkv.h."""
-    _dev(k_cache, "k_cache")
-    _dev(v_cache, "v_cache")
-    for n, t in (("block_tables", block_tables), ("context_lens", context_lens),
-                 ("query_start", query_start), ("accepted", accepted),
-                 ("num_accepted", num_accepted)):
-        _dev(t, n, torch.int32)
-    _same_device(k_cache, v_cache, block_tables, context_lens, query_start, accepted,
-                 num_accepted, dev_err)
+    _devs(("k_cache", "v_cache"), (k_cache, v_cache))
+    _devs(("block_tables", "context_lens", "query_start", "accepted", "num_accepted"),
+          (block_tables, context_lens, query_start, accepted, num_accepted), torch.int32)
+    _same_device(dev_err)
     if v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape:
         raise ValueError("k_cache and v_cache must match")
     num_blocks, hkv, bs, d = k_cache.shape
