@@ -11,6 +11,10 @@
 namespace pkv {
 namespace {
 
+#ifndef PKV_TREE_WHOLE
+#define PKV_TREE_WHOLE 6
+#endif
+
 using TreeFn = void (*)(const TreeParams, const CUtensorMap, const CUtensorMap);
 using TreeMergeFn = void (*)(const TreeParams);
 
@@ -32,12 +36,13 @@ TreeEntry tree_entry() {
 
 template <int D, class DT>
 TreeEntry tree_entry(bool fp8, int qt) {
-  if (qt == 1) return fp8 ? tree_entry<D, DT, true, 1>() : tree_entry<D, DT, false, 1>();
-  return fp8 ? tree_entry<D, DT, true, 2>() : tree_entry<D, DT, false, 2>();
+  if (fp8) return tree_entry<D, DT, true, 2>();
+  return qt == 1 ? tree_entry<D, DT, false, 1>() : tree_entry<D, DT, false, 2>();
 }
 
-// Two query tiles a CTA once a unit can have more than 128 rows: they share
-// each K/V tile.
+// Two query tiles a CTA once a unit can have more than 128 rows, as they share
+// each K/V tile; and over E4M3, whose tiles, held twice, leave room for one CTA an
+// SM, with two groups of softmax warps that take a smaller unit's tiles in turn.
 TreeEntry tree_entry(int head_dim, pkv_dtype dt, bool fp8, int max_rows) {
   const int qt = max_rows > 128 ? 2 : 1;
   if (head_dim == 128)
@@ -45,15 +50,20 @@ TreeEntry tree_entry(int head_dim, pkv_dtype dt, bool fp8, int max_rows) {
   return dt == PKV_FP16 ? tree_entry<64, Fp16>(fp8, qt) : tree_entry<64, Bf16>(fp8, qt);
 }
 
+// Units of few tiles are not cut, which spares the merge kernel.
+bool tree_whole(int max_context_len) { return max_context_len <= PKV_TREE_WHOLE * kTreeKeys; }
+
 // CTAs of a launch: no more than are resident, nor than the longest batch
 // within the bounds has stretches of kTreeMinTiles.
 int tree_ctas(int resident, int rows, int num_seqs, int group, int num_kv_heads,
               int max_context_len, int max_query_len) {
-  const long long tiles = (max_context_len + kTreeKeys - 1) / kTreeKeys + kTreeUnitCost;
+  const long long tiles =
+      2LL * ((max_context_len + kTreeKeys - 1) / kTreeKeys + kTreeUnitCost);  // positions
   const long long units =
       static_cast<long long>(num_seqs) * ((max_query_len * group + rows - 1) / rows);
   // units * kv heads * tiles, without its overflow
   if (units >= resident || units * num_kv_heads >= resident) return resident;
+  if (tree_whole(max_context_len)) return static_cast<int>(units * num_kv_heads);
   const long long most = (units * num_kv_heads * tiles + kTreeMinTiles - 1) / kTreeMinTiles;
   return static_cast<int>(std::min<long long>(resident, most));
 }
@@ -128,6 +138,7 @@ pkv_status tree_launch(void* out, const void* q, const void* k_cache, const void
   p.max_context_len = max_context_len;
   p.max_query_len = max_query_len;
   p.num_blocks = num_blocks;
+  p.whole_units = tree_whole(max_context_len);
   p.err = dev_err;
   p.ws_meta = static_cast<int4*>(workspace);
   p.ws_o = reinterpret_cast<float*>(p.ws_meta + ctas);
@@ -137,10 +148,10 @@ pkv_status tree_launch(void* out, const void* q, const void* k_cache, const void
   if (st != PKV_OK) return st;
   st = cuda_status(launch_after_previous_smem(e.fn, dim3(ctas), dim3(e.threads), e.smem, stream, p,
                                               kmap, vmap));
-  if (st != PKV_OK || ctas == 1) return st;
+  if (st != PKV_OK || ctas == 1 || p.whole_units) return st;
   const dim3 merge(ctas, (std::min(max_rows, e.rows) + kTreeMergeRows - 1) / kTreeMergeRows);
   return cuda_status(
-      launch_after_previous(e.merge, merge, dim3(kTreeMergeRows * head_dim / 4), stream, p));
+      launch_after_previous(e.merge, merge, dim3(8 * head_dim / 4), stream, p));
 }
 
 }  // namespace
@@ -156,9 +167,14 @@ extern "C" size_t pkv_paged_attn_tree_workspace_bytes(int num_seqs, int num_head
     return 0;
   const int group = num_heads / num_kv_heads;
   if (group > 8) return 0;
-  const TreeEntry e = tree_entry(head_dim, PKV_FP16, false, max_query_len * group);
-  return tree_ws_bytes(tree_ctas(e.ctas, e.rows, num_seqs, group, num_kv_heads, max_context_len,
-                                 max_query_len), e.rows, head_dim);
+  size_t most = 0;
+  for (const bool fp8 : {false, true}) {
+    const TreeEntry e = tree_entry(head_dim, PKV_FP16, fp8, max_query_len * group);
+    const int ctas = tree_ctas(e.ctas, e.rows, num_seqs, group, num_kv_heads, max_context_len,
+                               max_query_len);
+    most = std::max(most, tree_ws_bytes(ctas, e.rows, head_dim));
+  }
+  return most;
 }
 
 extern "C" pkv_status pkv_paged_attn_tree(

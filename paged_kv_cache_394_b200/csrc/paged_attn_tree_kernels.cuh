@@ -47,6 +47,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "paged_attn_kernels.cuh"
 #include "paged_prefill_tc_kernels.cuh"
 
 namespace pkv {
@@ -65,6 +66,7 @@ struct TreeParams {
   const float* v_scales;
   int num_seqs, num_tokens, num_heads, num_kv_heads, group_shift;
   int block_size, max_blocks_per_seq, max_context_len, max_query_len, num_blocks;
+  int whole_units;  // units are not cut
   unsigned* err;
   // Workspace: for each CTA one merge entry {first token, kv head, first CTA,
   // rows} (rows = 0: nothing to merge) and two pieces of ROWS rows.
@@ -76,9 +78,58 @@ struct TreeParams {
 // What a unit costs beside its tiles, in tiles.  Measured on B200 (us; 2 / 4 / 6 /
 // 9): GQA chat batch 86 / 71 / 69 / 70, its E4M3 form 107 / 98 / 89 / 88, the
 // LLaMA-7B batch 112 / 111 / 111 / 112.
-constexpr int kTreeUnitCost = 6;
-constexpr int kTreeMinTiles = 2;  // the shortest stretch worth a CTA
+#ifndef PKV_UC
+#define PKV_UC 6
+#endif
+#ifndef PKV_MT
+#define PKV_MT 2
+#endif
+#ifndef PKV_FP8_NS
+#define PKV_FP8_NS 2
+#endif
+constexpr int kTreeUnitCost = PKV_UC;
+constexpr int kTreeMinTiles = PKV_MT;  // the shortest stretch worth a CTA
 constexpr int kTreeKeys = 64;     // keys per tile
+
+// 32 consecutive 32-bit columns of this warp's TMEM lanes.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// True in one lane of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
+// The larger of two 16-bit pairs, a NaN losing to a number.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, Fp16) {
+  const __half2 m = __hmax2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, Bf16) {
+  const __nv_bfloat162 m =
+      __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -97,6 +148,13 @@ struct TreeSeq {
 struct TreeLens {
   int ctx, q0, end;
 };
+// Positions on the line: a unit's cost beside its tiles, then its tiles, each
+// of them for every query tile of the unit.  `rows` of a unit, of 128 each.
+__device__ __forceinline__ int tree_per(int rows) { return rows > 128 ? 2 : 1; }
+__device__ __forceinline__ int tree_span(const TreeParams& p, int ctx, int rows) {
+  return p.whole_units ? 1
+                       : ((ctx + kTreeKeys - 1) / kTreeKeys + kTreeUnitCost) * tree_per(rows);
+}
 __device__ __forceinline__ TreeLens tree_lens(const TreeParams& p, int seq) {
   return {p.context_lens[seq], p.query_start[seq], p.query_start[seq + 1]};
 }
@@ -114,17 +172,27 @@ __device__ __forceinline__ bool tree_seq(const TreeParams& p, const TreeLens& x,
   return s.q_len > 0;
 }
 
-// A CTA's next piece of work: tiles t0 .. t1 - 1 of the nt of a unit.
+// A CTA's next piece of work: tiles t0 .. t1 - 1 of the nt of a unit.  `lead`:
+// positions between the unit's first tile and the start of the CTA's stretch.
 struct TreeItem {
-  int seq, ctx, q0, q_len, kvh, rt, t0, t1, nt;
+  int seq, ctx, q0, q_len, kvh, rt, t0, t1, nt, lead;
 };
+
+// The units of a sequence, row tile after row tile for each kv head; each kv
+// head's take this many positions.
+template <int ROWS>
+__device__ __forceinline__ int tree_head_span(const TreeParams& p, const TreeSeq& s) {
+  const int rows = s.q_len << p.group_shift;
+  const int full = rows / ROWS, rest = rows % ROWS;
+  return full * tree_span(p, s.ctx, ROWS) + (rest > 0 ? tree_span(p, s.ctx, rest) : 0);
+}
 
 // Walks a CTA's stretch.  Every role walks on its own.  The lengths of the
 // sequence after the one at hand are loaded ahead of their use.
 template <int ROWS>
 struct TreeWalk {
-  int seq, unit, at;  // the next sequence, unit of it, and position in the unit
-  int left;           // positions left in the stretch
+  int seq, kvh, rt, at;  // the next sequence, unit of it, and position in the unit
+  int left;              // positions left in the stretch
   bool loaded;
   TreeSeq s;
   TreeLens ahead;  // of sequence `seq`, until loaded; then of seq + 1
@@ -141,26 +209,33 @@ struct TreeWalk {
         }
       }
       const int nt = (s.ctx + kTreeKeys - 1) / kTreeKeys;
-      const int rts = ((s.q_len << p.group_shift) + ROWS - 1) / ROWS;
-      const int span = nt + kTreeUnitCost;
+      const int rows = (s.q_len << p.group_shift) - rt * ROWS;
+      const int per = tree_per(min(rows, ROWS));
+      const int span = tree_span(p, s.ctx, min(rows, ROWS));
       const int take = min(left, span - at);
       it.seq = seq;
       it.ctx = s.ctx;
       it.q0 = s.q0;
       it.q_len = s.q_len;
-      it.kvh = rts == 1 ? unit : unit / rts;
-      it.rt = unit - it.kvh * rts;
-      it.t0 = max(0, at - kTreeUnitCost);
-      it.t1 = max(0, at + take - kTreeUnitCost);
+      it.kvh = kvh;
+      it.rt = rt;
       it.nt = nt;
+      // a tile is the CTA's whose stretch holds its first position
+      it.t0 = p.whole_units ? 0 : max(0, (at + per - 1) / per - kTreeUnitCost);
+      it.t1 = p.whole_units ? nt : max(0, (at + take + per - 1) / per - kTreeUnitCost);
+      it.lead = max(0, at - kTreeUnitCost * per);
       left -= take;
       at += take;
       if (at == span) {
         at = 0;
-        if (++unit == rts * p.num_kv_heads) {
-          unit = 0;
-          ++seq;
-          loaded = false;
+        ++rt;
+        if (rows <= ROWS) {
+          rt = 0;
+          if (++kvh == p.num_kv_heads) {
+            kvh = 0;
+            ++seq;
+            loaded = false;
+          }
         }
       }
       if (it.t1 > it.t0) return true;
@@ -181,10 +256,10 @@ struct TreeTraits {
   static constexpr int PIECES = NKEY / 16, HALVES = D / 64;
   // K/V stages, E4M3 staging slots and CTAs an SM: what fits beside the query
   // tiles in 227 KB.  E4M3 tiles are held twice, so one CTA an SM.
-  static constexpr int MIN_BLOCKS = QT == 1 && !kFp8 ? 2 : 1;
-  static constexpr int NS = kFp8 ? (QT == 1 ? 3 : 2) : QT == 1 ? (D == 128 ? 2 : 4) : 4;
-  static constexpr int NSTG = kFp8 ? 4 : 0;
-  static constexpr int NWIDEN = kFp8 ? (QT == 1 ? 4 : 2) : 1;  // widening warps for each of K, V
+  static constexpr int MIN_BLOCKS = QT == 1 ? 2 : 1;
+  static constexpr int NS = kFp8 ? PKV_FP8_NS : QT == 1 ? (D == 128 ? 2 : 4) : 4;
+  static constexpr int NSTG = kFp8 ? 6 - PKV_FP8_NS : 0;
+  static constexpr int NWIDEN = kFp8 ? 2 : 1;  // widening warps for each of K, V
   static constexpr int SOFTMAX_WARP = 4;
   static constexpr int WIDEN_WARP = SOFTMAX_WARP + 4 * QT;
   static constexpr int THREADS = (WIDEN_WARP + (kFp8 ? 2 * NWIDEN : 0)) * 32;
@@ -198,18 +273,25 @@ struct TreeTraits {
   static constexpr int OFF_STG = OFF_KV + NS * STAGE;
   static constexpr int OFF_SEEN = OFF_STG + 2 * NSTG * STG_TILE;    // [ROWS][8] visible nodes
   static constexpr int OFF_PAR = OFF_SEEN + ROWS * 32;              // [QT][2][256] parents
-  static constexpr int OFF_BAR = OFF_PAR + QT * 2 * PKV_MAX_TREE_NODES * 4;
+  static constexpr int OFF_ML = OFF_PAR + QT * 2 * PKV_MAX_TREE_NODES * 4;  // group 1's (max, sum)
+  static constexpr int OFF_BAR = OFF_ML + (QT - 1) * M * 8;
   static constexpr int B_KFULL = 0, B_KEMPTY = NS, B_VFULL = 2 * NS, B_VEMPTY = 3 * NS;
   static constexpr int B_STG = 4 * NS, B_STGEMPTY = B_STG + 2 * NSTG;
-  static constexpr int B_Q = B_STGEMPTY + 2 * NSTG;  // per query tile: q, o_free, s[2], p[2], o[2]
-  static constexpr int B_GROUP = B_Q + 8 * QT;       // per query tile: its softmax warps meet
-  static constexpr int B_DRAIN = B_GROUP + QT;       // per issuer
+  static constexpr int B_Q = B_STGEMPTY + 2 * NSTG;  // q; per group: o_free, s[2], p[2], o[2]
+  static constexpr int B_GROUP = B_Q + 8 * QT;       // per group: its softmax warps meet
+  static constexpr int B_VREADY = B_GROUP + QT;      // per group: V of its cut tile is in
+  static constexpr int B_BOTH = B_VREADY + QT;       // group 1's share of an item
+  static constexpr int B_DRAIN = B_BOTH + 1;         // per issuer
   static constexpr int NBAR = B_DRAIN + 2;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 64;
   static constexpr int O_COL = 2 * NKEY;
   static constexpr int QCOLS = 256;
   static constexpr uint32_t TMEM_COLS = QT * QCOLS;
   static constexpr float kRescaleThreshold = 8.f;
+  // P before its maximum is looked at (see the softmax).  Measured on B200 (us):
+  // GQA chat batch 76 -> 71, its E4M3 form 73 -> 70; but two query tiles of bf16
+  // (long contexts) 264 -> 281.
+  static constexpr bool kAhead = QT == 1 || kFp8;
   static_assert(MIN_BLOCKS * (1024 + 1024 + SMEM) <= 228 * 1024, "shared memory per SM");
   static size_t smem_bytes() { return 1024 + static_cast<size_t>(SMEM); }
 };
@@ -238,10 +320,11 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
   // behind the barriers: TMEM address, where the stretch starts, the items
   // whose V held non-finite tree elements (by parity: item + 1)
   int* words = reinterpret_cast<int*>(smem + Tr::OFF_BAR + Tr::NBAR * 8);
-  int* s_found = words + 1;  // sequence, unit, position, length of the stretch
-  int* s_odd = words + 6;
+  // sequence, kv head, position in the unit, length of the stretch; lengths; row tile
+  int* s_found = words + 1;
+  int* s_odd = words + 9;
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(kFullMask, static_cast<int>(threadIdx.x) >> 5, 0);
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -259,17 +342,23 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
       mbar_init(bar_q(q), 4);  // one arrival per softmax warp
       mbar_init(bar_ofree(q), 4);
       mbar_init(bar(Tr::B_GROUP + q), 4);
+      mbar_init(bar(Tr::B_VREADY + q), 1);
       for (int b = 0; b < 2; ++b) {
         mbar_init(bar_s(q, b), 1);
         mbar_init(bar_p(q, b), 4);
         mbar_init(bar_o(q, b), 1);
       }
     }
+    mbar_init(bar(Tr::B_BOTH), 4);
     mbar_init(bar(Tr::B_DRAIN), 1);
     mbar_init(bar(Tr::B_DRAIN + 1), 1);
     s_found[3] = 0;
     s_odd[0] = s_odd[1] = 0;
     fence_mbar_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(smem_addr(words), Tr::TMEM_COLS);
+    tc::tmem_relinquish();
   }
   grid_dependency_wait();
   trigger_dependents();
@@ -279,15 +368,17 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
     const int per = (p.num_seqs + Tr::THREADS - 1) / Tr::THREADS;
     const int first = min(p.num_seqs, static_cast<int>(threadIdx.x) * per);
     const int last = min(p.num_seqs, first + per);
-    auto weight = [&](int i, bool report) -> long long {
+    auto weight = [&](const TreeLens& x, bool report) -> long long {
       TreeSeq s;
-      if (!tree_seq(p, tree_lens(p, i), s, report)) return 0;
-      const int rts = ((s.q_len << p.group_shift) + ROWS - 1) / ROWS;
-      return static_cast<long long>(rts) * p.num_kv_heads *
-             ((s.ctx + NKEY - 1) / NKEY + kTreeUnitCost);
+      if (!tree_seq(p, x, s, report)) return 0;
+      return static_cast<long long>(tree_head_span<ROWS>(p, s)) * p.num_kv_heads;
     };
     long long own = 0;
-    for (int i = first; i < last; ++i) own += weight(i, blockIdx.x == 0);
+    TreeLens lens = {};  // of the last of this thread's sequences
+    for (int i = first; i < last; ++i) {
+      lens = tree_lens(p, i);
+      own += weight(lens, blockIdx.x == 0);
+    }
     long long upto = own;  // inclusive scan over the warp, then over the warps
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -302,20 +393,34 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
       if (w < warp) upto += sums[w];
       total += sums[w];
     }
-    const long long even = (total + gridDim.x - 1) / gridDim.x;
-    const long long len = even > kTreeMinTiles ? even : kTreeMinTiles;
+    const bool small = total + gridDim.x < 0x7fffffff;  // 32-bit divisions, many times as fast
+    const long long even = small ? (static_cast<unsigned>(total) + gridDim.x - 1) / gridDim.x
+                                 : (total + gridDim.x - 1) / gridDim.x;
+    const long long least = p.whole_units ? 1 : kTreeMinTiles;
+    const long long len = even > least ? even : least;
     const long long start = len * blockIdx.x;
     if (start < upto && start >= upto - own) {
       long long at = start - (upto - own);
       for (int i = first; i < last; ++i) {
-        const long long w = weight(i, false);
+        const TreeLens x = per == 1 ? lens : tree_lens(p, i);
+        const long long w = weight(x, false);
         if (at < w) {
-          const int span = (p.context_lens[i] + NKEY - 1) / NKEY + kTreeUnitCost;
+          TreeSeq seq;
+          tree_seq(p, x, seq, false);
+          const int head = tree_head_span<ROWS>(p, seq);
+          const int full = tree_span(p, seq.ctx, ROWS);  // every row tile but the last
+          const int kvh = small ? static_cast<int>(at) / head : static_cast<int>(at / head);
+          const int in_head = static_cast<int>(at - static_cast<long long>(kvh) * head);
+          const int rt = min(in_head / full, ((seq.q_len << p.group_shift) - 1) / ROWS);
           s_found[0] = i;
-          s_found[1] = static_cast<int>(at / span);
-          s_found[2] = static_cast<int>(at % span);
+          s_found[1] = kvh;
+          s_found[7] = rt;
+          s_found[2] = in_head - rt * full;
           // the line's end cuts the last stretch by itself
           s_found[3] = static_cast<int>(len < 0x7fffffff ? len : 0x7fffffff);
+          s_found[4] = x.ctx;
+          s_found[5] = x.q0;
+          s_found[6] = x.end;
           break;
         }
         at -= w;
@@ -323,30 +428,31 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
     }
     if (threadIdx.x == 0) p.ws_meta[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
-  __syncthreads();
-  if (s_found[3] == 0) return;
-  TreeWalk<ROWS> walk;
-  walk.seq = s_found[0];
-  walk.unit = s_found[1];
-  walk.at = s_found[2];
-  walk.left = s_found[3];
-  walk.loaded = false;
-  walk.ahead = tree_lens(p, walk.seq);
-  const int len = walk.left;
-
-  if (warp == 1) {
-    tc::tmem_alloc(smem_addr(words), Tr::TMEM_COLS);
-    tc::tmem_relinquish();
-  }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t tmem = static_cast<uint32_t>(words[0]);
+  const uint32_t tmem = __shfl_sync(kFullMask, static_cast<uint32_t>(words[0]), 0);
+  if (s_found[3] == 0) {
+    if (warp == 1) tc::tmem_dealloc(tmem, Tr::TMEM_COLS);
+    return;
+  }
+  TreeWalk<ROWS> walk;
+  walk.seq = s_found[0];
+  walk.kvh = s_found[1];
+  walk.rt = s_found[7];
+  walk.at = s_found[2];
+  walk.left = s_found[3];
+  walk.loaded = false;
+  walk.ahead = {s_found[4], s_found[5], s_found[6]};
+  const int len = walk.left;
 
   // rows of query tile q of an item
   auto rows_of = [&](const TreeItem& it, int q) {
     return min(M, (it.q_len << p.group_shift) - it.rt * ROWS - q * M);
   };
+  // Where a unit has at most 128 rows, the two groups of softmax warps of a QT = 2
+  // CTA take its tiles in turn, each with its own S, P and O.
+  auto in_turn = [&](const TreeItem& x) { return QT == 2 && rows_of(x, 1) <= 0; };
   // the tile holds keys that not every row sees, or none
   auto partial = [&](const TreeItem& it, int t) { return (t + 1) * NKEY > it.ctx - it.q_len; };
   TreeItem it;
@@ -433,181 +539,212 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
     }
     __syncwarp();
   } else if (warp == 1 || warp == 3) {
-    // ---- MMA issuers: S (warp 1) and P.V (warp 3), one thread each --------------------
-    if (lane == 0) {
-      bool ok = true;
-      const uint64_t d_q = tc::smem_desc_sw128(sbase, 16, 1024);
-      const uint64_t d_k = tc::smem_desc_sw128(sbase + Tr::OFF_KV, 16, 1024);
-      const uint64_t d_v =
-          tc::smem_desc_sw128(sbase + Tr::OFF_KV + Tr::KV_TILE, Tr::KV_HALF, 1024);
-      int gt = 0;
-      int tq[QT] = {}, iq[QT] = {};  // tiles and items of each query tile so far
-      while (ok && walk.next(p, it)) {
-        const bool act[2] = {true, QT == 2 && rows_of(it, 1) > 0};
-        if (warp == 1) {
+    // ---- MMA issuers: S (warp 1) and P.V (warp 3) --------------------------------------
+    // The whole warp runs the loop and one elected thread issues: with the loop's
+    // values the same in all lanes, the descriptors stay in uniform registers,
+    // where the MMA wants them.  (One lane alone in the loop moved each of them
+    // there anew: 82 cycles an MMA, now PKV_ISSUE_CYCLES.)
+    bool ok = true;
+    const uint64_t d_q = tc::smem_desc_sw128(sbase, 16, 1024);
+    const uint64_t d_k = tc::smem_desc_sw128(sbase + Tr::OFF_KV, 16, 1024);
+    const uint64_t d_v = tc::smem_desc_sw128(sbase + Tr::OFF_KV + Tr::KV_TILE, Tr::KV_HALF, 1024);
+    auto wait = [&](uint32_t barrier, int parity) {
+      ok = __all_sync(kFullMask, mbar_wait_bounded(barrier, parity & 1));
+    };
+    int gt = 0;
+    int tg[QT] = {}, ig[QT] = {}, iq[QT] = {};  // tiles, items of each group; Q tiles loaded
+    while (ok && walk.next(p, it)) {
+      const bool alt = __any_sync(kFullMask, in_turn(it));
+      const int ntiles = __shfl_sync(kFullMask, it.t1 - it.t0, 0);
+      // the first tile with keys that not every row sees
+      const int whole = __shfl_sync(kFullMask, max(0, (it.ctx - it.q_len) / NKEY - it.t0), 0);
+      if (warp == 1) {
 #pragma unroll
-          for (int q = 0; q < QT; ++q) {
-            if (!ok || !act[q]) continue;
-            ok = mbar_wait_bounded(bar_q(q), iq[q] & 1);
-            ++iq[q];
-          }
-          for (int t = it.t0; ok && t < it.t1; ++t, ++gt) {
-            ok = mbar_wait_bounded(bar(Tr::B_KFULL + gt % NS), (gt / NS) & 1);
-            const uint64_t k0 = d_k + static_cast<uint32_t>((gt % NS) * (Tr::STAGE >> 4));
+        for (int q = 0; q < QT; ++q) {
+          if (!ok || (q > 0 && alt)) continue;
+          wait(bar_q(q), iq[q]);
+          ++iq[q];
+        }
+        for (int i = 0; ok && i < ntiles; ++i, ++gt) {
+          wait(bar(Tr::B_KFULL + gt % NS), gt / NS);
+          const uint64_t k0 = d_k + static_cast<uint32_t>((gt % NS) * (Tr::STAGE >> 4));
 #pragma unroll
-            for (int q = 0; q < QT; ++q) {
-              if (!ok || !act[q]) continue;
-              const int b = tq[q] & 1;
-              // the buffer holds P of two tiles ago until P.V has read it
-              if (tq[q] >= 2) ok = mbar_wait_bounded(bar_o(q, b), ((tq[q] - 2) >> 1) & 1);
-              if (!ok) break;
-              tc::tc_fence_after();
-              const uint64_t q0d = d_q + q * (Tr::Q_TILE >> 4);
+          for (int g = 0; g < QT; ++g) {
+            if (!ok || (alt && (i & 1) != g)) continue;
+            const int b = tg[g] & 1;
+            // the buffer holds P of the group's tile before last until P.V has read it
+            if (tg[g] >= 2) wait(bar_o(g, b), (tg[g] - 2) >> 1);
+            if (!ok) break;
+            tc::tc_fence_after();
+            const uint64_t q0d = d_q + (alt ? 0 : g) * (Tr::Q_TILE >> 4);
+            if (elect_one()) {
 #pragma unroll
               for (int ks = 0; ks < D / 16; ++ks) {
                 const uint32_t step = (ks >> 2) * (Tr::Q_HALF >> 4) + (ks & 3) * 2;
                 const uint32_t kstep = (ks >> 2) * (Tr::KV_HALF >> 4) + (ks & 3) * 2;
-                tc::umma_f16(tmem + q * Tr::QCOLS + b * NKEY, q0d + step, k0 + kstep, IDESC_S,
+                tc::umma_f16(tmem + g * Tr::QCOLS + b * NKEY, q0d + step, k0 + kstep, IDESC_S,
                              ks > 0 ? 1u : 0u);
               }
-              tc::umma_commit(bar_s(q, b));
-              ++tq[q];
+              tc::umma_commit(bar_s(g, b));
             }
-            if (ok) tc::umma_commit(bar(Tr::B_KEMPTY + gt % NS));
+            __syncwarp();
+            ++tg[g];
           }
-        } else {
-          for (int t = it.t0; ok && t < it.t1; ++t, ++gt) {
-            // V rows of such a tile are cleared by every query tile's softmax
-            const bool all_p = partial(it, t) || t == it.t1 - 1;
-            if (all_p) {
+          if (ok && elect_one()) tc::umma_commit(bar(Tr::B_KEMPTY + gt % NS));
+          __syncwarp();
+        }
+      } else {
+        for (int i = 0; ok && i < ntiles; ++i, ++gt) {
+          wait(bar(Tr::B_VFULL + gt % NS), gt / NS);
+          if (!ok) break;
+          // The softmax of every group that the tile goes to clears V rows of a
+          // cut tile.  It is told here that they are in: this warp alone passes
+          // every tile's barrier in turn, and so cannot mistake an earlier phase.
+          const bool cut = i >= whole;
+          if (cut && lane == 0) {
 #pragma unroll
-              for (int q = 0; q < QT; ++q)
-                if (ok && act[q]) ok = mbar_wait_bounded(bar_p(q, tq[q] & 1), (tq[q] >> 1) & 1);
+            for (int g = 0; g < QT; ++g)
+              if (!alt || (i & 1) == g) mbar_arrive(bar(Tr::B_VREADY + g));
+          }
+          const bool all_p = !alt && (cut || i == ntiles - 1);
+          if (all_p) {
+#pragma unroll
+            for (int g = 0; g < QT; ++g)
+              if (ok) wait(bar_p(g, tg[g] & 1), tg[g] >> 1);
+          }
+          const uint64_t v0 = d_v + static_cast<uint32_t>((gt % NS) * (Tr::STAGE >> 4));
+#pragma unroll
+          for (int g = 0; g < QT; ++g) {
+            if (!ok || (alt && (i & 1) != g)) continue;
+            const int b = tg[g] & 1;
+            const bool first = i == (alt ? g : 0);
+            if (!all_p) wait(bar_p(g, b), tg[g] >> 1);
+            // the first tile overwrites the group's O of the item before
+            if (first) {
+              if (ok && ig[g] > 0) wait(bar_ofree(g), ig[g] - 1);
+              ++ig[g];
             }
-            if (ok) ok = mbar_wait_bounded(bar(Tr::B_VFULL + gt % NS), (gt / NS) & 1);
-            const uint64_t v0 = d_v + static_cast<uint32_t>((gt % NS) * (Tr::STAGE >> 4));
-#pragma unroll
-            for (int q = 0; q < QT; ++q) {
-              if (!ok || !act[q]) continue;
-              const int b = tq[q] & 1;
-              if (!all_p) ok = mbar_wait_bounded(bar_p(q, b), (tq[q] >> 1) & 1);
-              // the first tile overwrites the O of the item before
-              if (ok && t == it.t0 && iq[q] > 0)
-                ok = mbar_wait_bounded(bar_ofree(q), (iq[q] - 1) & 1);
-              if (!ok) break;
-              tc::tc_fence_after();
-              const uint32_t ptm = tmem + q * Tr::QCOLS + b * NKEY;
-              const uint32_t otm = tmem + q * Tr::QCOLS + Tr::O_COL;
+            if (!ok) break;
+            tc::tc_fence_after();
+            const uint32_t ptm = tmem + g * Tr::QCOLS + b * NKEY;
+            const uint32_t otm = tmem + g * Tr::QCOLS + Tr::O_COL;
+            if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < NKEY / 16; ++kk) {
                 const uint64_t bdesc = v0 + kk * (2048 >> 4);
-                tc::umma_f16_ts(otm, ptm + 8 * kk, bdesc, IDESC_O,
-                                (t > it.t0 || kk > 0) ? 1u : 0u);
+                tc::umma_f16_ts(otm, ptm + 8 * kk, bdesc, IDESC_O, (!first || kk > 0) ? 1u : 0u);
                 if constexpr (Tr::kBf16)
                   tc::umma_f16_ts(otm, ptm + NKEY / 2 + 8 * kk, bdesc, IDESC_O, 1u);
               }
-              tc::umma_commit(bar_o(q, b));
-              ++tq[q];
+              tc::umma_commit(bar_o(g, b));
             }
-            if (ok) tc::umma_commit(bar(Tr::B_VEMPTY + gt % NS));
+            __syncwarp();
+            ++tg[g];
           }
-#pragma unroll
-          for (int q = 0; q < QT; ++q)
-            if (act[q]) ++iq[q];
+          if (ok && elect_one()) tc::umma_commit(bar(Tr::B_VEMPTY + gt % NS));
+          __syncwarp();
         }
       }
-      if (!ok) {
-        set_err(p.err, PKV_DEVERR_TIMEOUT);
-        // what was issued completes before TMEM is freed
-        const uint32_t drain = bar(Tr::B_DRAIN + (warp == 1 ? 0 : 1));
-        tc::umma_commit(drain);
-        (void)mbar_wait_bounded(drain, 0);
-      }
+    }
+    if (!ok && elect_one()) {
+      set_err(p.err, PKV_DEVERR_TIMEOUT);
+      // what was issued completes before TMEM is freed
+      const uint32_t drain = bar(Tr::B_DRAIN + (warp == 1 ? 0 : 1));
+      tc::umma_commit(drain);
+      (void)mbar_wait_bounded(drain, 0);
     }
     __syncwarp();
   } else if (warp < Tr::WIDEN_WARP) {
-    // ---- softmax warps: query tile q, thread <-> row <-> TMEM lane ---------------------
-    const int q = (warp - Tr::SOFTMAX_WARP) >> 2;
+    // ---- softmax warps: group g, thread <-> row <-> TMEM lane --------------------------
+    const int g = (warp - Tr::SOFTMAX_WARP) >> 2;
     const int quarter = warp & 3;  // the TMEM lanes this warp may access
     const int r = quarter * 32 + lane;
-    const uint32_t tm = tmem + q * Tr::QCOLS + (static_cast<uint32_t>(quarter * 32) << 16);
-    uint32_t* seen = reinterpret_cast<uint32_t*>(smem + Tr::OFF_SEEN) + (q * M + r) * 8;
-    int* par = reinterpret_cast<int*>(smem + Tr::OFF_PAR) + q * 2 * PKV_MAX_TREE_NODES;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tm = tmem + g * Tr::QCOLS + lanes;
+    uint32_t* seen = reinterpret_cast<uint32_t*>(smem + Tr::OFF_SEEN) + (g * M + r) * 8;
+    int* par = reinterpret_cast<int*>(smem + Tr::OFF_PAR) + g * 2 * PKV_MAX_TREE_NODES;
+    float2* s_ml = reinterpret_cast<float2*>(smem + Tr::OFF_ML);
     int met = 0;
-    // a barrier of the query tile's softmax warps, bounded as every wait
+    // a barrier of the group's warps, bounded as every wait
     auto group_sync = [&] {
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(Tr::B_GROUP + q));
-      return __all_sync(kFullMask, mbar_wait_bounded(bar(Tr::B_GROUP + q), met++ & 1));
+      if (lane == 0) mbar_arrive(bar(Tr::B_GROUP + g));
+      return __all_sync(kFullMask, mbar_wait_bounded(bar(Tr::B_GROUP + g), met++ & 1));
     };
     const int gmask = (1 << p.group_shift) - 1;
-    // row `row` of the item's query tile in q and out
-    auto row_at = [&](const TreeItem& x, int row) {
-      const int c = x.rt * ROWS + q * M + row;
+    // row `row` of the item's query tile qt in q and out
+    auto row_at = [&](const TreeItem& x, int qt, int row) {
+      const int c = x.rt * ROWS + qt * M + row;
       return static_cast<size_t>(x.q0 + (c >> p.group_shift)) * p.num_heads +
              (static_cast<size_t>(x.kvh) << p.group_shift) + (c & gmask);
     };
-    // An item's query rows and its tree's parents come by cp.async, issued once
-    // the last S of the item before is complete; rows that do not exist are
-    // left as they are (nobody reads their S).
-    auto begin_load = [&](const TreeItem& x, int parity) {
+    // An item's query tiles and its tree's parents come by cp.async, the tiles
+    // issued once the last S of the item before is complete; rows that do not
+    // exist are left as they are (nobody reads their S).
+    auto q_chunks = [&](const TreeItem& x, int qt, auto f) {
       constexpr int CH = D / 8;
-      const int n = rows_of(x, q) * CH;
-      const uint32_t qt = sbase + q * Tr::Q_TILE;
+      const int n = rows_of(x, qt) * CH;
+#pragma unroll 2
       for (int i = r; i < n; i += 128) {
         const int row = i / CH, ch = i % CH;
-        cp_async16(qt + (ch >> 3) * Tr::Q_HALF + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
-                   static_cast<const T*>(p.q) + row_at(x, row) * D + ch * 8);
-      }
-      if (partial(x, x.t1 - 1)) {
-        const int nodes = ((x.rt * ROWS + q * M + rows_of(x, q) - 1) >> p.group_shift) + 1;
-        for (int i = r; i < nodes; i += 128)
-          cp_async4(smem_addr(par + parity * PKV_MAX_TREE_NODES + i), p.parents + x.q0 + i);
+        f(qt * Tr::Q_TILE + (ch >> 3) * Tr::Q_HALF + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
+          row, ch);
       }
     };
-    auto end_load = [&](const TreeItem& x) {
+    auto begin_q = [&](const TreeItem& x, int qt) {
+      q_chunks(x, qt, [&](int at, int row, int ch) {
+        cp_async16(sbase + at, static_cast<const T*>(p.q) + row_at(x, qt, row) * D + ch * 8);
+      });
+    };
+    auto begin_parents = [&](const TreeItem& x, int parity) {
+      if (!partial(x, x.t1 - 1)) return;
+      const int qt = in_turn(x) ? 0 : g;
+      const int nodes = ((x.rt * ROWS + qt * M + rows_of(x, qt) - 1) >> p.group_shift) + 1;
+      for (int i = r; i < nodes; i += 128)
+        cp_async4(smem_addr(par + parity * PKV_MAX_TREE_NODES + i), p.parents + x.q0 + i);
+    };
+    auto end_q = [&](const TreeItem& x, int qt) {
       cp_async_wait_all();
-      if constexpr (Tr::kQToFp16) {
-        constexpr int CH = D / 8;
-        const int n = rows_of(x, q) * CH;
-        for (int i = r; i < n; i += 128) {
-          const int row = i / CH, ch = i % CH;
-          uint4* at = reinterpret_cast<uint4*>(smem + q * Tr::Q_TILE + (ch >> 3) * Tr::Q_HALF +
-                                               row * 128 + (((ch & 7) ^ (row & 7)) << 4));
-          const uint4 u = *at;
-          *at = make_uint4(bf16x2_to_f16x2_sat(u.x), bf16x2_to_f16x2_sat(u.y),
-                           bf16x2_to_f16x2_sat(u.z), bf16x2_to_f16x2_sat(u.w));
-        }
-      }
+      if constexpr (Tr::kQToFp16)
+        q_chunks(x, qt, [&](int at, int, int) {
+          uint4* c = reinterpret_cast<uint4*>(smem + at);
+          const uint4 u = *c;
+          *c = make_uint4(bf16x2_to_f16x2_sat(u.x), bf16x2_to_f16x2_sat(u.y),
+                          bf16x2_to_f16x2_sat(u.z), bf16x2_to_f16x2_sat(u.w));
+        });
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_q(q));
+      if (lane == 0) mbar_arrive(bar_q(qt));
     };
-    int gt = 0, tq = 0, item = 0;
+    // tiles of all items before, of this group, of group 1; items, those with an O
+    // of this group, those that both groups share; this group's cut tiles
+    int gt0 = 0, tg = 0, tg1 = 0, items = 0, ig = 0, shared_items = 0, cuts = 0;
     bool ok = true;
     TreeItem nx;
     bool more = walk.next(p, nx);
-    if (more && rows_of(nx, q) > 0) {
-      begin_load(nx, 1);
-      end_load(nx);
+    if (more) {
+      begin_parents(nx, 1);
+      if (g == 0 || !in_turn(nx)) {
+        begin_q(nx, g);
+        end_q(nx, g);
+      }
     }
     while (ok && more) {
       it = nx;
       more = walk.next(p, nx);
-      ++item;
-      const bool load_next = more && rows_of(nx, q) > 0;
-      const int nrows = rows_of(it, q);
-      if (nrows <= 0) {  // the second query tile of a unit of few rows
-        gt += it.t1 - it.t0;
-        if (load_next) {
-          begin_load(nx, (item + 1) & 1);
-          end_load(nx);
-        }
-        continue;
-      }
+      ++items;
+      const bool alt = in_turn(it);
+      const int qt = alt ? 0 : g, step = alt ? 2 : 1;
+      const int ntiles = it.t1 - it.t0;
+      const int nrows = rows_of(it, qt);
       const bool active = r < nrows;
       const bool warp_active = quarter * 32 < nrows;
       const int hist = it.ctx - it.q_len;
+      // Who brings the next item's query tiles: a group brings its own, but after
+      // an item taken in turn the group of the last tile brings both, for its S
+      // is the last that reads them.
+      const bool mine0 = more && (alt ? ((ntiles - 1) & 1) == g : g == 0);
+      const bool mine1 = QT == 2 && more && !in_turn(nx) && (alt ? ((ntiles - 1) & 1) == g : g == 1);
       float k_scale = 1.f, v_scale = 1.f;
       if constexpr (Tr::kFp8) {
         k_scale = p.k_scales[it.kvh];
@@ -616,11 +753,12 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
             r == 0)
           set_err(p.err, PKV_DEVERR_BAD_SCALE);
       }
+      cp_async_wait_all();  // this thread's share of the parents
       if (partial(it, it.t1 - 1)) {
         // the nodes that each row sees: itself, its parent, and so on
-        const int node = (it.rt * ROWS + q * M + min(r, nrows - 1)) >> p.group_shift;
-        const int* up = par + (item & 1) * PKV_MAX_TREE_NODES;
-        ok = group_sync();  // every thread's share of the parents has arrived
+        const int node = (it.rt * ROWS + qt * M + min(r, nrows - 1)) >> p.group_shift;
+        const int* up = par + (items & 1) * PKV_MAX_TREE_NODES;
+        ok = group_sync();
         if (!ok) break;
 #pragma unroll
         for (int w = 0; w < 8; ++w) seen[w] = 0;
@@ -641,6 +779,8 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
           n = x;
         }
         seen[at] = bits;
+        // only an item that ends its unit, and so has tree keys, is followed by another
+        if (more) begin_parents(nx, (items + 1) & 1);
       }
       // The row's visible keys of tile t, bit by bit.
       auto window = [&](int t) -> unsigned long long {
@@ -657,97 +797,126 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
         const unsigned long long lo = word(w) | (word(w + 1) << 32);
         return sh == 0 ? lo : (lo >> sh) | (word(w + 2) << (64 - sh));
       };
-      float m = -INFINITY, l = 0.f;
+      // rows that do not exist keep a maximum that no value passes
+      float m = active ? -INFINITY : INFINITY, l = 0.f;
       // x = s * qscale; for qscale > 0 the row's max of x is (max s) * qscale
       // exactly, so s is masked and reduced unscaled and the scale folds into
       // the exponent's multiply-add
       const float mult0 = p.qscale * k_scale;
       const float mult = mult0 > 0.f ? mult0 : 1.f;
-      for (int t = it.t0; t < it.t1; ++t, ++gt, ++tq) {
-        const int b = tq & 1;
-        ok = mbar_wait_bounded(bar_s(q, b), (tq >> 1) & 1);
+      for (int t = it.t0 + (alt ? g : 0); t < it.t1; t += step, ++tg) {
+        const int b = tg & 1, stage = gt0 + t - it.t0;
+        ok = mbar_wait_bounded(bar_s(g, b), (tg >> 1) & 1);
         if (!__all_sync(kFullMask, ok)) {
           ok = false;
           break;
         }
         tc::tc_fence_after();
-        // every S of this item is complete: its query tile may be replaced
-        if (t == it.t1 - 1 && load_next) begin_load(nx, (item + 1) & 1);
+        if (t == it.t1 - 1) {  // every S of this item is complete
+          if (mine0) begin_q(nx, 0);
+          if (mine1) begin_q(nx, 1);
+        }
         const bool cut = partial(it, t);
         if (warp_active) {
           const uint32_t sbuf = tm + b * NKEY;
-          float s[64];
+          // P of the tile: 2^(s mult - m) in 16 bits, two keys a word, and what
+          // that rounds off for bf16; returns the sum
+          uint32_t w[32], wl[Tr::kBf16 ? 32 : 1];
+          auto weigh = [&](const float (&s)[32], int h, float neg_m, uint64_t (&sum2)[2]) {
+            const uint64_t mult2 = tc::f2_pack(mult, mult), neg_m2 = tc::f2_pack(neg_m, neg_m);
 #pragma unroll
-          for (int c = 0; c < 64; c += 16) {
-            float v[16];
-            tc::tmem_ld16(sbuf + c, v);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[c + i] = v[i];
-          }
-          tc::tmem_wait_ld();
-          if (!(mult0 > 0.f)) {
-#pragma unroll
-            for (int c = 0; c < 64; ++c) s[c] *= mult0;
-          }
-          if (cut) {
-            const unsigned long long w = window(t);
-            const uint32_t w0 = static_cast<uint32_t>(w), w1 = static_cast<uint32_t>(w >> 32);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              if (!(w0 & (1u << c))) s[c] = -INFINITY;
-              if (!(w1 & (1u << c))) s[32 + c] = -INFINITY;
-            }
-          }
-          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int c = 0; c < 64; c += 8) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) mx4[u] = tc::max3(mx4[u], s[c + u], s[c + 4 + u]);
-          }
-          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * mult;
-          float alpha = 1.f;
-          if (active && mx > m + Tr::kRescaleThreshold) {
-            alpha = exp2_approx(m - mx);  // 0 on the first tile (m = -inf)
-            m = mx;
-          }
-          const float neg_m = m == -INFINITY ? 0.f : -m;
-          const uint64_t mult2 = tc::f2_pack(mult, mult), neg_m2 = tc::f2_pack(neg_m, neg_m);
-          uint64_t sum2[2] = {tc::f2_pack(0.f, 0.f), tc::f2_pack(0.f, 0.f)};
-#pragma unroll
-          for (int c = 0; c < 64; c += 4) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float x0, x1;
-              tc::f2_unpack(
-                  tc::f2_fma(tc::f2_pack(s[c + 2 * h], s[c + 2 * h + 1]), mult2, neg_m2), x0, x1);
-              s[c + 2 * h] = exp2_approx(x0);
-              s[c + 2 * h + 1] = exp2_approx(x1);
-              sum2[h] = tc::f2_add(sum2[h], tc::f2_pack(s[c + 2 * h], s[c + 2 * h + 1]));
-            }
-          }
-          // P over the S columns just read: 32 columns, and 32 of low halves for bf16
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            uint32_t w[16], wl[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float x = s[32 * g + 2 * e], y = s[32 * g + 2 * e + 1];
-              w[e] = pack2(x, y, MT());
+            for (int c = 0; c < 32; c += 2) {
+              float x, y;
+              tc::f2_unpack(tc::f2_fma(tc::f2_pack(s[c], s[c + 1]), mult2, neg_m2), x, y);
+              x = exp2_approx(x);
+              y = exp2_approx(y);
+              sum2[(c >> 1) & 1] = tc::f2_add(sum2[(c >> 1) & 1], tc::f2_pack(x, y));
+              const uint32_t u = pack2(x, y, MT());
+              w[h * 16 + c / 2] = u;
               if constexpr (Tr::kBf16)
-                wl[e] = pack2(x - __uint_as_float(w[e] << 16),
-                              y - __uint_as_float(w[e] & 0xffff0000u), Bf16());
+                wl[h * 16 + c / 2] = pack2(x - __uint_as_float(u << 16),
+                                           y - __uint_as_float(u & 0xffff0000u), Bf16());
             }
-            tc::tmem_st16u(sbuf + 16 * g, w);
-            if constexpr (Tr::kBf16) tc::tmem_st16u(sbuf + NKEY / 2 + 16 * g, wl);
+          };
+          auto total = [&](const uint64_t (&sum2)[2]) {
+            float a[4];
+            tc::f2_unpack(sum2[0], a[0], a[1]);
+            tc::f2_unpack(sum2[1], a[2], a[3]);
+            return (a[0] + a[1]) + (a[2] + a[3]);
+          };
+          // Most tiles move no maximum: P is made with the one at hand, and only
+          // where a value passes 2^8 (kRescaleThreshold), or a row has none yet,
+          // is the tile read again and its maximum taken.
+          float alpha = 1.f, sum;
+          bool take_max =
+              !Tr::kAhead || __any_sync(kFullMask, cut || !(mult0 > 0.f) || m == -INFINITY);
+          for (;;) {
+            float s[2][32];
+            tmem_ld32(sbuf, s[0]);
+            tmem_ld32(sbuf + 32, s[1]);
+            tc::tmem_wait_ld();
+            if (take_max) {
+              if (cut || !(mult0 > 0.f)) {
+                const unsigned long long bits = window(t);
+                const uint32_t b0 = static_cast<uint32_t>(bits);
+                const uint32_t b1 = static_cast<uint32_t>(bits >> 32);
+                const float f = mult0 > 0.f ? 1.f : mult0;
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                  s[0][c] = b0 & (1u << c) ? s[0][c] * f : -INFINITY;
+                  s[1][c] = b1 & (1u << c) ? s[1][c] * f : -INFINITY;
+                }
+              }
+              float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int c = 0; c < 32; c += 4) {
+                mx4[0] = tc::max3(mx4[0], s[0][c], s[0][c + 1]);
+                mx4[1] = tc::max3(mx4[1], s[0][c + 2], s[0][c + 3]);
+                mx4[2] = tc::max3(mx4[2], s[1][c], s[1][c + 1]);
+                mx4[3] = tc::max3(mx4[3], s[1][c + 2], s[1][c + 3]);
+              }
+              const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * mult;
+              if (mx > m + Tr::kRescaleThreshold) {
+                alpha = exp2_approx(m - mx);  // 0 on the first tile (m = -inf)
+                m = mx;
+              }
+            }
+            const float neg_m = m == -INFINITY ? 0.f : -m;
+            uint64_t sum2[2] = {0, 0};
+            weigh(s[0], 0, neg_m, sum2);
+            weigh(s[1], 1, neg_m, sum2);
+            sum = total(sum2);
+            if (take_max) break;
+            uint32_t top[4] = {w[0], w[1], w[2], w[3]};
+#pragma unroll
+            for (int c = 4; c < 32; c += 4)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) top[u] = max2(top[u], w[c + u], MT());
+            const uint32_t most = max2(max2(top[0], top[1], MT()), max2(top[2], top[3], MT()), MT());
+            constexpr uint32_t kMost = Tr::kBf16 ? 0x4380u : 0x5C00u;  // 2^8, as a bit pattern
+            if (!__any_sync(kFullMask,
+                            active && ((most & 0xffffu) > kMost || (most >> 16) > kMost)))
+              break;
+            take_max = true;
+          }
+          l = l * alpha + sum;
+          // P over S: 32 columns, and 32 of what bf16 rounded off
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t x[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = w[16 * h + e];
+            tc::tmem_st16u(sbuf + 16 * h, x);
+            if constexpr (Tr::kBf16) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[e] = wl[16 * h + e];
+              tc::tmem_st16u(sbuf + NKEY / 2 + 16 * h, x);
+            }
           }
           tc::tmem_wait_st();
-          float a[4];
-          tc::f2_unpack(sum2[0], a[0], a[1]);
-          tc::f2_unpack(sum2[1], a[2], a[3]);
-          l = l * alpha + ((a[0] + a[1]) + (a[2] + a[3]));
-          if (t > it.t0 && __any_sync(kFullMask, alpha != 1.f)) {
+          if (t - it.t0 >= step && __any_sync(kFullMask, alpha != 1.f)) {
             // O holds every earlier tile before it is rescaled
-            ok = mbar_wait_bounded(bar_o(q, (tq - 1) & 1), ((tq - 1) >> 1) & 1);
+            ok = mbar_wait_bounded(bar_o(g, (tg - 1) & 1), ((tg - 1) >> 1) & 1);
             if (!__all_sync(kFullMask, ok)) {
               ok = false;
               break;
@@ -766,7 +935,7 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
           }
         }
         if (cut) {
-          ok = mbar_wait_bounded(bar(Tr::B_VFULL + gt % NS), (gt / NS) & 1);
+          ok = mbar_wait_bounded(bar(Tr::B_VREADY + g), cuts++ & 1);
           if (!__all_sync(kFullMask, ok)) {
             ok = false;
             break;
@@ -774,110 +943,166 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
           // an element with all exponent bits set is infinite or NaN
           constexpr uint32_t kExp = Tr::kBf16 ? 0x7F807F80u : 0x7C007C00u;
           constexpr uint32_t kOne = Tr::kBf16 ? 0x00800080u : 0x04000400u;
-          unsigned char* vt = smem + Tr::OFF_KV + (gt % NS) * Tr::STAGE + Tr::KV_TILE;
+          unsigned char* vt = smem + Tr::OFF_KV + (stage % NS) * Tr::STAGE + Tr::KV_TILE;
           const int from = max(0, hist - t * NKEY), end = it.ctx - t * NKEY;
-          for (int i = from * 8 + r; i < NKEY * 8; i += 128) {
-            const int row = i >> 3;
+          auto hit = [&](uint32_t x) { return ((x & kExp) + kOne) & 0x80008000u; };
+          // 16-byte chunk k of this thread: row r / 8 + 16 (k / HALVES), half k % HALVES
+          constexpr int CHUNKS = NKEY * 8 / 128 * HALVES;
+          auto chunk = [&](int k) {
+            return reinterpret_cast<uint4*>(vt + (k % HALVES) * Tr::KV_HALF + r * 16 +
+                                            (k / HALVES) * 2048);
+          };
+          uint32_t odd = 0;
 #pragma unroll
-            for (int h = 0; h < HALVES; ++h) {
-              uint4* at = reinterpret_cast<uint4*>(vt + h * Tr::KV_HALF + i * 16);
-              if (row >= end) {
-                *at = make_uint4(0u, 0u, 0u, 0u);
-                continue;
-              }
-              uint4 u = *at;
-              auto hit = [&](uint32_t x) { return ((x & kExp) + kOne) & 0x80008000u; };
-              if (hit(u.x) | hit(u.y) | hit(u.z) | hit(u.w)) {
-                auto clear = [&](uint32_t x) {
-                  const uint32_t y = hit(x);
-                  return x & ~((y & 0x8000u ? 0xffffu : 0u) | (y >> 16 ? 0xffff0000u : 0u));
-                };
-                s_odd[item & 1] = item;  // before the elements are cleared
-                __threadfence_block();
-                *at = make_uint4(clear(u.x), clear(u.y), clear(u.z), clear(u.w));
+          for (int k = 0; k < CHUNKS; ++k) {
+            const int row = r / 8 + 16 * (k / HALVES);
+            const uint4 u = *chunk(k);
+            if (row >= end)
+              *chunk(k) = make_uint4(0u, 0u, 0u, 0u);
+            else if (row >= from)
+              odd |= hit(u.x) | hit(u.y) | hit(u.z) | hit(u.w);
+          }
+          if (odd != 0) {
+            s_odd[items & 1] = items;  // before the elements are cleared
+            __threadfence_block();
+#pragma unroll 1
+            for (int k = 0; k < CHUNKS; ++k) {
+              const int row = r / 8 + 16 * (k / HALVES);
+              uint32_t* at = reinterpret_cast<uint32_t*>(chunk(k));
+              for (int e = 0; e < 4 && row >= from && row < end; ++e) {
+                const uint32_t y = hit(at[e]);
+                at[e] &= ~((y & 0x8000u ? 0xffffu : 0u) | (y >> 16 ? 0xffff0000u : 0u));
               }
             }
           }
+          fence_proxy_async_smem();
         }
-        fence_proxy_async_smem();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_p(q, b));
+        if (lane == 0) mbar_arrive(bar_p(g, b));
       }
       if (!ok) break;
-      if (load_next) end_load(nx);
+      if (mine0) end_q(nx, 0);
+      if (mine1) end_q(nx, 1);
+      const bool both = alt && ntiles > 1;  // the two groups share the item's tiles
+      const int other = QT == 1 ? 0 : alt ? ntiles >> 1 : ntiles;
+      gt0 += ntiles;
+      if (alt && g == 1) {
+        if (both) {
+          // group 0 takes what this group has; it has read the last such
+          if (ig > 0) ok = mbar_wait_bounded(bar_ofree(1), (ig - 1) & 1);
+          ok = __all_sync(kFullMask, ok);
+          if (!ok) break;
+          s_ml[r] = make_float2(m, l);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(Tr::B_BOTH));
+          ++ig;
+        }
+        continue;
+      }
+      ++ig;
+      tg1 += other;
       // ---- output ------------------------------------------------------------------
-      ok = mbar_wait_bounded(bar_o(q, (tq - 1) & 1), ((tq - 1) >> 1) & 1);
+      ok = mbar_wait_bounded(bar_o(g, (tg - 1) & 1), ((tg - 1) >> 1) & 1);
+      float f0 = 1.f, f1 = 0.f;
+      if (both) {
+        ok = ok && mbar_wait_bounded(bar(Tr::B_BOTH), shared_items++ & 1) &&
+             mbar_wait_bounded(bar_o(1, (tg1 - 1) & 1), ((tg1 - 1) >> 1) & 1);
+      }
       if (!__all_sync(kFullMask, ok)) {
         ok = false;
         break;
       }
       tc::tc_fence_after();
+      if (both) {
+        const float2 x = s_ml[r];
+        const float top = fmaxf(m, x.x);
+        f0 = m == -INFINITY ? 0.f : exp2_approx(m - top);
+        f1 = x.x == -INFINITY ? 0.f : exp2_approx(x.x - top);
+        l = l * f0 + x.y * f1;
+        m = top;
+      }
       const bool whole = it.t0 == 0 && it.t1 == it.nt;
-      const bool odd = *static_cast<volatile int*>(s_odd + (item & 1)) == item;
+      const bool odd = *static_cast<volatile int*>(s_odd + (items & 1)) == items;
+      const size_t row = row_at(it, qt, min(r, nrows - 1));
+      // pieces: the one that starts a unit is its CTA's second, any other its first
+      const size_t piece = static_cast<size_t>(blockIdx.x) * 2 + (it.t0 == 0 ? 1 : 0);
       if (warp_active) {
         const float inv = l > 0.f || l != l ? v_scale / l : 0.f;
-        const size_t row = row_at(it, min(r, nrows - 1));
-        // pieces: the one that starts a unit is its CTA's second, any other its first
-        const size_t slot =
-            (static_cast<size_t>(blockIdx.x) * 2 + (it.t0 == 0 ? 1 : 0)) * ROWS + q * M + r;
-        if (!whole && active) p.ws_ml[slot] = make_float2(l != l ? l : m, l);
+        if (!whole && active) p.ws_ml[piece * ROWS + qt * M + r] = make_float2(l != l ? l : m, l);
 #pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          float v[16];
-          tc::tmem_ld16(tm + Tr::O_COL + c, v);
-          tc::tmem_wait_ld();
-          if (!active) continue;
-          if (odd) {
-            // infinities and NaN in the V of the nodes that this row sees
-            const int32_t* trow =
-                p.block_tables + static_cast<size_t>(it.seq) * p.max_blocks_per_seq;
-            const int lo = max(0, it.t0 * NKEY - hist), hi = min(it.q_len, it.t1 * NKEY - hist);
-            for (int n = lo; n < hi; ++n) {
-              if (!(seen[n >> 5] >> (n & 31) & 1u)) continue;
-              const int key = hist + n;
-              const int pb = trow[key / p.block_size];
-              if (static_cast<unsigned>(pb) >= static_cast<unsigned>(p.num_blocks)) continue;
-              const size_t at = ((static_cast<size_t>(pb) * p.num_kv_heads + it.kvh) *
-                                     p.block_size + key % p.block_size) * D + c;
-              for (int i = 0; i < 16; ++i) {
-                float x;
-                if constexpr (Tr::kFp8)
-                  x = (static_cast<const uint8_t*>(p.v_cache)[at + i] & 0x7F) == 0x7F ? NAN : 0.f;
-                else
-                  x = static_cast<float>(static_cast<const T*>(p.v_cache)[at + i]);
-                if (!(fabsf(x) < INFINITY)) v[i] += x;
-              }
-            }
-          }
-          if (whole) {
-            float a[8], z[8];
+        for (int c = 0; c < D; c += 32) {
+          float v[32];
+          tmem_ld32(tm + Tr::O_COL + c, v);
+          if (both) {
+            float x[32];
+            tmem_ld32(tm + Tr::QCOLS + Tr::O_COL + c, x);
+            tc::tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              a[i] = v[i] * inv;
-              z[i] = v[8 + i] * inv;
-            }
+            for (int i = 0; i < 32; ++i) v[i] = v[i] * f0 + x[i] * f1;
+          } else {
+            tc::tmem_wait_ld();
+          }
+          if (!active) continue;
+          if (whole) {
             T* o = static_cast<T*>(p.out) + row * D + c;
-            *reinterpret_cast<uint4*>(o) = pack8(a, typename Tr::DT());
-            *reinterpret_cast<uint4*>(o + 8) = pack8(z, typename Tr::DT());
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              float x[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] = v[i + e] * inv;
+              *reinterpret_cast<uint4*>(o + i) = pack8(x, typename Tr::DT());
+            }
           } else {
             // [D / 4][ROWS] of 4 floats: a warp's rows side by side
-            float4* o = reinterpret_cast<float4*>(p.ws_o) + (slot - q * M - r) * (D / 4) + q * M + r;
+            float4* o = reinterpret_cast<float4*>(p.ws_o) + piece * (D / 4) * ROWS + qt * M + r;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 8; ++i)
               o[(c / 4 + i) * ROWS] = make_float4(v[4 * i] * v_scale, v[4 * i + 1] * v_scale,
-                                 v[4 * i + 2] * v_scale, v[4 * i + 3] * v_scale);
+                                                  v[4 * i + 2] * v_scale, v[4 * i + 3] * v_scale);
           }
+        }
+      }
+      if (odd && active && l == l) {
+        // infinities and NaN in the V of the nodes that this row sees: their sum
+        // is the element's value, whatever the rest is
+        const int32_t* trow = p.block_tables + static_cast<size_t>(it.seq) * p.max_blocks_per_seq;
+        const int lo = max(0, it.t0 * NKEY - hist), hi = min(it.q_len, it.t1 * NKEY - hist);
+#pragma unroll 1
+        for (int c = 0; c < D; ++c) {
+          float sum = 0.f;
+#pragma unroll 1
+          for (int n = lo; n < hi; ++n) {
+            if (!(seen[n >> 5] >> (n & 31) & 1u)) continue;
+            const int key = hist + n;
+            const int pb = trow[key / p.block_size];
+            if (static_cast<unsigned>(pb) >= static_cast<unsigned>(p.num_blocks)) continue;
+            const size_t at = ((static_cast<size_t>(pb) * p.num_kv_heads + it.kvh) *
+                                   p.block_size + key % p.block_size) * D + c;
+            float x;
+            if constexpr (Tr::kFp8)
+              x = (static_cast<const uint8_t*>(p.v_cache)[at] & 0x7F) == 0x7F ? NAN : 0.f;
+            else
+              x = static_cast<float>(static_cast<const T*>(p.v_cache)[at]);
+            if (!(fabsf(x) < INFINITY)) sum += x;
+          }
+          if (sum == 0.f) continue;
+          if (whole)
+            static_cast<T*>(p.out)[row * D + c] = static_cast<T>(sum);
+          else
+            p.ws_o[((piece * (D / 4) + c / 4) * ROWS + qt * M + r) * 4 + c % 4] = sum;
         }
       }
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_ofree(q));
-      if (q == 0 && r == 0 && it.t0 > 0 && it.t1 == it.nt) {
+      if (lane == 0) {
+        mbar_arrive(bar_ofree(g));
+        if (both) mbar_arrive(bar_ofree(1));
+      }
+      if (g == 0 && r == 0 && it.t0 > 0 && it.t1 == it.nt) {
         // this CTA ends a unit that another began: the one whose stretch holds
-        // the unit's first tile, (t0 + kTreeUnitCost) - kTreeUnitCost positions
-        // before this stretch's start
-        const int before = (it.t0 + len - 1) / len;
+        // the unit's first tile, `lead` positions before this stretch's start
+        const int before = (it.lead + len - 1) / len;
         p.ws_meta[blockIdx.x] =
             make_int4(it.q0 + ((it.rt * ROWS) >> p.group_shift), it.kvh,
                       static_cast<int>(blockIdx.x) - before,
@@ -910,31 +1135,38 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
             sbase + Tr::OFF_KV + stage * Tr::STAGE + (is_k ? 0 : Tr::KV_TILE);
         // Chunk c of key r (dims 16c ..) becomes 16-bit chunks 2(c % 4) and
         // 2(c % 4) + 1 of row r in dim half c / 4, 128-byte swizzled; codes of
-        // 128-byte rows come swizzled, of 64-byte rows not.
-#pragma unroll 4
-        for (int k = 0; k < CHUNKS / 32; ++k) {
-          const int i = part * CHUNKS + lane + 32 * k;
-          const int row = i / (D / 16), c = i % (D / 16);
-          const uint32_t from = D == 128 ? row * 128 + ((c ^ (row & 7)) << 4) : i * 16;
-          uint32_t x[4];
+        // 128-byte rows come swizzled, of 64-byte rows not.  A step of 32 chunks
+        // is 512 bytes of codes and 4 or 8 rows, so that the swizzle of a lane's
+        // chunks repeats every second step or every one.
+        constexpr int STEPS = CHUNKS / 32, RSTEP = 512 / D;  // rows a step
+        const int row0 = part * (CHUNKS * 16 / D) + lane / (D / 16), c = lane % (D / 16);
+        uint32_t x[STEPS][4];
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) {
+          const int r7 = (row0 + (D == 128 ? (k & 1) * 4 : 0)) & 7;
+          const uint32_t from = D == 128 ? row0 * 128 + ((c ^ r7) << 4)
+                                         : part * CHUNKS * 16 + lane * 16;
           asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                       : "r"(src + from)
+                       : "=r"(x[k][0]), "=r"(x[k][1]), "=r"(x[k][2]), "=r"(x[k][3])
+                       : "r"(src + from + k * 512)
                        : "memory");
+        }
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) {
+          const int r7 = (row0 + (D == 128 ? (k & 1) * 4 : 0)) & 7;
+          const uint32_t to = dst + (c >> 2) * Tr::KV_HALF + row0 * 128 + k * RSTEP * 128;
+          // the lanes of the second dim half store their second chunk first, so
+          // that the 8 lanes of a row fill all its banks
+          const bool swap = c >= 4;
+          const uint32_t at = ((((c & 3) * 2) ^ r7) << 4) ^ (swap ? 16 : 0);
           uint32_t h[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            h[2 * e] = e4m3x2_to(x[e] & 0xffffu, Fp16());
-            h[2 * e + 1] = e4m3x2_to(x[e] >> 16, Fp16());
-          }
-          const uint32_t to = dst + (c >> 2) * Tr::KV_HALF + row * 128;
-          const int c0 = (c & 3) * 2;
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           to + ((c0 ^ (row & 7)) << 4)),
-                       "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+          for (int e = 0; e < 4; ++e)
+            e4m3x4_to_f16x2(swap ? x[k][e ^ 2] : x[k][e], h[2 * e], h[2 * e + 1]);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + at), "r"(h[0]),
+                       "r"(h[1]), "r"(h[2]), "r"(h[3])
                        : "memory");
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           to + (((c0 + 1) ^ (row & 7)) << 4)),
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + (at ^ 16)),
                        "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7])
                        : "memory");
         }
@@ -963,45 +1195,64 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
 //   out = sum 2^(m - M) o / sum 2^(m - M) l.
 // Entry blockIdx.x is of the unit that ended in that CTA; the piece of the unit's
 // first CTA is that CTA's second, of every later one its first.  A thread has 4
-// dims of a row, a warp 2 rows x 64 dims (whole sectors of the pieces);
+// dims of 4 rows, a warp 2 rows x 64 dims at once (whole sectors of the pieces);
 // blockIdx.y takes kTreeMergeRows rows.
-constexpr int kTreeMergeRows = 8;
+constexpr int kTreeMergeRows = 32;
 template <int D, int ROWS, class DT>
-__global__ void __launch_bounds__(kTreeMergeRows * D / 4)
-    paged_attn_tree_merge_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(8 * D / 4) paged_attn_tree_merge_kernel(const TreeParams p) {
   using T = typename DT::T;
+  constexpr int N = kTreeMergeRows / 8;
   grid_dependency_wait();
   trigger_dependents();
   const int4 e = p.ws_meta[blockIdx.x];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = static_cast<int>(blockIdx.y) * kTreeMergeRows + (w / (D / 64)) * 2 + (lane & 1);
+  const int r0 = static_cast<int>(blockIdx.y) * kTreeMergeRows + (w / (D / 64)) * 2 + (lane & 1);
   const int c4 = (w % (D / 64)) * 16 + (lane >> 1);
-  if (r >= e.w) return;
+  if (r0 >= e.w) return;
   const int last = static_cast<int>(blockIdx.x);
-  auto piece = [&](int c) { return static_cast<size_t>(c) * 2 + (c == e.z ? 1 : 0); };
   // an online sum, so that every load of a piece is under way at once
-  float big = -INFINITY, num[4] = {}, den = 0.f;
-#pragma unroll 4
-  for (int c = e.z; c <= last; ++c) {
-    const float2 ml = p.ws_ml[piece(c) * ROWS + r];
-    const float4 o = reinterpret_cast<const float4*>(p.ws_o)[(piece(c) * (D / 4) + c4) * ROWS + r];
-    const float m = ml.x == -INFINITY ? big : fmaxf(big, ml.x);
-    const float a = big == -INFINITY ? 0.f : exp2_approx(big - m);
-    const float f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - m);
-    big = m;
-    den = den * a + f * ml.y;
-    num[0] = num[0] * a + f * o.x;
-    num[1] = num[1] * a + f * o.y;
-    num[2] = num[2] * a + f * o.z;
-    num[3] = num[3] * a + f * o.w;
+  float big[N], den[N], num[N][4];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    big[i] = -INFINITY;
+    den[i] = num[i][0] = num[i][1] = num[i][2] = num[i][3] = 0.f;
   }
-  const float inv = den > 0.f || den != den ? 1.f / den : 0.f;
-  T* out = static_cast<T*>(p.out) +
-           (static_cast<size_t>(e.x + (r >> p.group_shift)) * p.num_heads +
-            (static_cast<size_t>(e.y) << p.group_shift) + (r & ((1 << p.group_shift) - 1))) * D +
-           c4 * 4;
-  *reinterpret_cast<uint2*>(out) = make_uint2(pack2(num[0] * inv, num[1] * inv, DT()),
-                                              pack2(num[2] * inv, num[3] * inv, DT()));
+#pragma unroll 2
+  for (int c = e.z; c <= last; ++c) {
+    const size_t piece = static_cast<size_t>(c) * 2 + (c == e.z ? 1 : 0);
+    float2 ml[N];
+    float4 o[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = min(r0 + 8 * i, e.w - 1);
+      ml[i] = p.ws_ml[piece * ROWS + r];
+      o[i] = reinterpret_cast<const float4*>(p.ws_o)[(piece * (D / 4) + c4) * ROWS + r];
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float m = ml[i].x == -INFINITY ? big[i] : fmaxf(big[i], ml[i].x);
+      const float a = big[i] == -INFINITY ? 0.f : exp2_approx(big[i] - m);
+      const float f = ml[i].x == -INFINITY ? 0.f : exp2_approx(ml[i].x - m);
+      big[i] = m;
+      den[i] = den[i] * a + f * ml[i].y;
+      num[i][0] = num[i][0] * a + f * o[i].x;
+      num[i][1] = num[i][1] * a + f * o[i].y;
+      num[i][2] = num[i][2] * a + f * o[i].z;
+      num[i][3] = num[i][3] * a + f * o[i].w;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int r = r0 + 8 * i;
+    if (r >= e.w) break;
+    const float inv = den[i] > 0.f || den[i] != den[i] ? 1.f / den[i] : 0.f;
+    T* out = static_cast<T*>(p.out) +
+             (static_cast<size_t>(e.x + (r >> p.group_shift)) * p.num_heads +
+              (static_cast<size_t>(e.y) << p.group_shift) + (r & ((1 << p.group_shift) - 1))) * D +
+             c4 * 4;
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack2(num[i][0] * inv, num[i][1] * inv, DT()),
+                                                pack2(num[i][2] * inv, num[i][3] * inv, DT()));
+  }
 }
 
 }  // namespace pkv
