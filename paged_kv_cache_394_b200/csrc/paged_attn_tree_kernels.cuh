@@ -67,6 +67,8 @@ struct TreeParams {
   int num_seqs, num_tokens, num_heads, num_kv_heads, group_shift;
   int block_size, max_blocks_per_seq, max_context_len, max_query_len, num_blocks;
   int whole_units;  // units are not cut
+  int direct;       // ... and each has its CTA: max_rts for every (sequence, kv head)
+  int max_rts;
   unsigned* err;
   // Workspace: for each CTA one merge entry {first token, kv head, first CTA,
   // rows} (rows = 0: nothing to merge) and two pieces of ROWS rows.
@@ -364,7 +366,25 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
   trigger_dependents();
 
   // ---- where this CTA's stretch of the line starts -------------------------------
-  {
+  TreeWalk<ROWS> walk;
+  int len, early = -1;  // early: the first table entries, where the sequence is known at once
+  if (p.direct) {
+    // a CTA per unit, without the scan
+    const int units = p.num_kv_heads * p.max_rts;
+    walk.seq = static_cast<int>(blockIdx.x) / units;
+    walk.kvh = static_cast<int>(blockIdx.x) % units / p.max_rts;
+    walk.rt = static_cast<int>(blockIdx.x) % p.max_rts;
+    walk.ahead = tree_lens(p, walk.seq);
+    walk.at = 0;
+    if ((warp == 0 || warp == 2) && lane < p.max_blocks_per_seq)
+      early = p.block_tables[static_cast<size_t>(walk.seq) * p.max_blocks_per_seq + lane];
+    TreeSeq s;
+    len = tree_seq(p, walk.ahead, s,
+                   static_cast<int>(blockIdx.x) % units == 0 && threadIdx.x == 0) &&
+          walk.rt * ROWS < s.q_len << p.group_shift;
+    tc::tc_fence_before();
+    __syncthreads();
+  } else {
     const int per = (p.num_seqs + Tr::THREADS - 1) / Tr::THREADS;
     const int first = min(p.num_seqs, static_cast<int>(threadIdx.x) * per);
     const int last = min(p.num_seqs, first + per);
@@ -397,8 +417,8 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
     const long long even = small ? (static_cast<unsigned>(total) + gridDim.x - 1) / gridDim.x
                                  : (total + gridDim.x - 1) / gridDim.x;
     const long long least = p.whole_units ? 1 : kTreeMinTiles;
-    const long long len = even > least ? even : least;
-    const long long start = len * blockIdx.x;
+    const long long each = even > least ? even : least;
+    const long long start = each * blockIdx.x;
     if (start < upto && start >= upto - own) {
       long long at = start - (upto - own);
       for (int i = first; i < last; ++i) {
@@ -417,7 +437,7 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
           s_found[7] = rt;
           s_found[2] = in_head - rt * full;
           // the line's end cuts the last stretch by itself
-          s_found[3] = static_cast<int>(len < 0x7fffffff ? len : 0x7fffffff);
+          s_found[3] = static_cast<int>(each < 0x7fffffff ? each : 0x7fffffff);
           s_found[4] = x.ctx;
           s_found[5] = x.q0;
           s_found[6] = x.end;
@@ -427,24 +447,23 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
       }
     }
     if (threadIdx.x == 0) p.ws_meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+    tc::tc_fence_before();
+    __syncthreads();
+    walk.seq = s_found[0];
+    walk.kvh = s_found[1];
+    walk.rt = s_found[7];
+    walk.at = s_found[2];
+    walk.ahead = {s_found[4], s_found[5], s_found[6]};
+    len = s_found[3];
   }
-  tc::tc_fence_before();
-  __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = __shfl_sync(kFullMask, static_cast<uint32_t>(words[0]), 0);
-  if (s_found[3] == 0) {
+  if (len == 0) {
     if (warp == 1) tc::tmem_dealloc(tmem, Tr::TMEM_COLS);
     return;
   }
-  TreeWalk<ROWS> walk;
-  walk.seq = s_found[0];
-  walk.kvh = s_found[1];
-  walk.rt = s_found[7];
-  walk.at = s_found[2];
-  walk.left = s_found[3];
+  walk.left = len;
   walk.loaded = false;
-  walk.ahead = {s_found[4], s_found[5], s_found[6]};
-  const int len = walk.left;
 
   // rows of query tile q of an item
   auto rows_of = [&](const TreeItem& it, int q) {
@@ -479,18 +498,18 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
     const int shift = p.block_size == 16 ? 4 : 5;
     int gt = 0;
     bool ok = true;
-    // 32 entries of an item's table row at a time, an item's first ones while
-    // the item before it is under way
+    // 32 entries of an item's table row at a time (those past the context are
+    // not used), an item's first ones while the item before it is under way
     auto entries = [&](const TreeItem& x, int chunk) {
       const int i = (chunk << 5) + lane;
-      return i < (x.ctx + p.block_size - 1) >> shift
+      return i < p.max_blocks_per_seq
                  ? p.block_tables[static_cast<size_t>(x.seq) * p.max_blocks_per_seq + i]
                  : -1;
     };
     auto first_chunk = [&](const TreeItem& x) { return (x.t0 * NKEY) >> (shift + 5); };
     TreeItem nx;
     bool more = walk.next(p, nx);
-    int ahead = more ? entries(nx, first_chunk(nx)) : -1;
+    int ahead = p.direct ? early : more ? entries(nx, first_chunk(nx)) : -1;
     while (ok && more) {
       it = nx;
       int chunk = first_chunk(it), entry = ahead;
@@ -1195,63 +1214,53 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
 //   out = sum 2^(m - M) o / sum 2^(m - M) l.
 // Entry blockIdx.x is of the unit that ended in that CTA; the piece of the unit's
 // first CTA is that CTA's second, of every later one its first.  A thread has 4
-// dims of 4 rows, a warp 2 rows x 64 dims at once (whole sectors of the pieces);
-// blockIdx.y takes kTreeMergeRows rows.
-constexpr int kTreeMergeRows = 32;
+// dims of a row, a warp 2 rows x 64 dims (whole sectors of the pieces), a block
+// 8 rows, blockIdx.y of them first and every gridDim.y-th; 8 pieces' loads are
+// under way at once.
 template <int D, int ROWS, class DT>
 __global__ void __launch_bounds__(8 * D / 4) paged_attn_tree_merge_kernel(const TreeParams p) {
   using T = typename DT::T;
-  constexpr int N = kTreeMergeRows / 8;
   grid_dependency_wait();
   trigger_dependents();
   const int4 e = p.ws_meta[blockIdx.x];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r0 = static_cast<int>(blockIdx.y) * kTreeMergeRows + (w / (D / 64)) * 2 + (lane & 1);
   const int c4 = (w % (D / 64)) * 16 + (lane >> 1);
-  if (r0 >= e.w) return;
   const int last = static_cast<int>(blockIdx.x);
-  // an online sum, so that every load of a piece is under way at once
-  float big[N], den[N], num[N][4];
+  for (int r = static_cast<int>(blockIdx.y) * 8 + (w / (D / 64)) * 2 + (lane & 1); r < e.w;
+       r += 8 * gridDim.y) {
+    float big = -INFINITY, num[4] = {}, den = 0.f;
+    constexpr int N = 8;
+    for (int c0 = e.z; c0 <= last; c0 += N) {
+      float2 ml[N];
+      float4 o[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    big[i] = -INFINITY;
-    den[i] = num[i][0] = num[i][1] = num[i][2] = num[i][3] = 0.f;
-  }
-#pragma unroll 2
-  for (int c = e.z; c <= last; ++c) {
-    const size_t piece = static_cast<size_t>(c) * 2 + (c == e.z ? 1 : 0);
-    float2 ml[N];
-    float4 o[N];
+      for (int i = 0; i < N; ++i) {
+        const int c = min(c0 + i, last);
+        const size_t piece = static_cast<size_t>(c) * 2 + (c == e.z ? 1 : 0);
+        ml[i] = p.ws_ml[piece * ROWS + r];
+        o[i] = reinterpret_cast<const float4*>(p.ws_o)[(piece * (D / 4) + c4) * ROWS + r];
+      }
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int r = min(r0 + 8 * i, e.w - 1);
-      ml[i] = p.ws_ml[piece * ROWS + r];
-      o[i] = reinterpret_cast<const float4*>(p.ws_o)[(piece * (D / 4) + c4) * ROWS + r];
+      for (int i = 0; i < N; ++i) {
+        if (c0 + i > last) break;
+        const float m = ml[i].x == -INFINITY ? big : fmaxf(big, ml[i].x);
+        const float a = big == -INFINITY ? 0.f : exp2_approx(big - m);
+        const float f = ml[i].x == -INFINITY ? 0.f : exp2_approx(ml[i].x - m);
+        big = m;
+        den = den * a + f * ml[i].y;
+        num[0] = num[0] * a + f * o[i].x;
+        num[1] = num[1] * a + f * o[i].y;
+        num[2] = num[2] * a + f * o[i].z;
+        num[3] = num[3] * a + f * o[i].w;
+      }
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float m = ml[i].x == -INFINITY ? big[i] : fmaxf(big[i], ml[i].x);
-      const float a = big[i] == -INFINITY ? 0.f : exp2_approx(big[i] - m);
-      const float f = ml[i].x == -INFINITY ? 0.f : exp2_approx(ml[i].x - m);
-      big[i] = m;
-      den[i] = den[i] * a + f * ml[i].y;
-      num[i][0] = num[i][0] * a + f * o[i].x;
-      num[i][1] = num[i][1] * a + f * o[i].y;
-      num[i][2] = num[i][2] * a + f * o[i].z;
-      num[i][3] = num[i][3] * a + f * o[i].w;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int r = r0 + 8 * i;
-    if (r >= e.w) break;
-    const float inv = den[i] > 0.f || den[i] != den[i] ? 1.f / den[i] : 0.f;
+    const float inv = den > 0.f || den != den ? 1.f / den : 0.f;
     T* out = static_cast<T*>(p.out) +
              (static_cast<size_t>(e.x + (r >> p.group_shift)) * p.num_heads +
               (static_cast<size_t>(e.y) << p.group_shift) + (r & ((1 << p.group_shift) - 1))) * D +
              c4 * 4;
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack2(num[i][0] * inv, num[i][1] * inv, DT()),
-                                                pack2(num[i][2] * inv, num[i][3] * inv, DT()));
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack2(num[0] * inv, num[1] * inv, DT()),
+                                                pack2(num[2] * inv, num[3] * inv, DT()));
   }
 }
 
