@@ -14,14 +14,19 @@
 // SMs, so up to 128 rows a unit is bound by memory and QT = 1 (one 128-row query
 // tile) runs two CTAs an SM, one's softmax under the other's loads.  More rows
 // take QT = 2: two query tiles share each K/V tile, one CTA an SM, bound by
-// softmax and MMA.
+// softmax and MMA.  E4M3 caches take QT = 2 always: their tiles lie in shared
+// memory twice, as codes and as fp16, so one CTA fits, and its two groups of
+// softmax warps take the tiles of a unit of up to 128 rows in turn.  What bounds
+// them is shared memory: codes in, out and back as fp16, and the MMAs' reads are
+// about 130 KB a tile, 1024 cycles at 128 bytes each, where HBM needs 705.
 //
 // Split: the tiles of all units lie on one line, every sequence's units one
 // after the other, and CTA c takes the c-th of gridDim.x equal stretches of it,
 // whatever the lengths.  (A unit counts kTreeUnitCost tiles more than it has,
 // for its query tile, pipeline fill and output.)  A unit that lies in one
 // stretch is written out directly; pieces of a cut unit go to the workspace as
-// (max, sum, unnormalised o) and paged_attn_tree_merge_kernel joins them.
+// (max, sum, unnormalised o) and paged_attn_tree_merge_kernel joins them.  Units of
+// few tiles are left whole (tree_whole in paged_attn_tree.cu).
 //
 // A CTA: warp 0 / 2 bring K / V tiles by TMA through the block table into a
 // ring of NS stages; warp 1 issues S = Q K^T into one of two TMEM buffers; warp
@@ -77,20 +82,13 @@ struct TreeParams {
   float* ws_o;    // [pieces][D / 4][ROWS][4]
 };
 
-// What a unit costs beside its tiles, in tiles.  Measured on B200 (us; 2 / 4 / 6 /
-// 9): GQA chat batch 86 / 71 / 69 / 70, its E4M3 form 107 / 98 / 89 / 88, the
-// LLaMA-7B batch 112 / 111 / 111 / 112.
-#ifndef PKV_UC
-#define PKV_UC 6
-#endif
-#ifndef PKV_MT
-#define PKV_MT 2
-#endif
-#ifndef PKV_FP8_NS
-#define PKV_FP8_NS 2
-#endif
-constexpr int kTreeUnitCost = PKV_UC;
-constexpr int kTreeMinTiles = PKV_MT;  // the shortest stretch worth a CTA
+// What a unit costs beside its tiles, in tiles.  Measured on B200 (us; 4 / 5 / 6):
+// GQA chat batch 74.1 / 73.4 / 72.2, the LLaMA-7B batch 104.4 / 104.6 / 105.7, the
+// E4M3 batch 77.7 / 75.8 / 75.4.
+constexpr int kTreeUnitCost = 6;
+// The shortest stretch worth a CTA (2 / 6: one sequence of 1200 tokens 15.3 / 15.9
+// us, batches alike).
+constexpr int kTreeMinTiles = 2;
 constexpr int kTreeKeys = 64;     // keys per tile
 
 // 32 consecutive 32-bit columns of this warp's TMEM lanes.
@@ -259,8 +257,8 @@ struct TreeTraits {
   // K/V stages, E4M3 staging slots and CTAs an SM: what fits beside the query
   // tiles in 227 KB.  E4M3 tiles are held twice, so one CTA an SM.
   static constexpr int MIN_BLOCKS = QT == 1 ? 2 : 1;
-  static constexpr int NS = kFp8 ? PKV_FP8_NS : QT == 1 ? (D == 128 ? 2 : 4) : 4;
-  static constexpr int NSTG = kFp8 ? 6 - PKV_FP8_NS : 0;
+  static constexpr int NS = kFp8 ? 2 : QT == 1 ? (D == 128 ? 2 : 4) : 4;
+  static constexpr int NSTG = kFp8 ? 4 : 0;  // (3 stages and 3 slots measured the same)
   static constexpr int NWIDEN = kFp8 ? 2 : 1;  // widening warps for each of K, V
   static constexpr int SOFTMAX_WARP = 4;
   static constexpr int WIDEN_WARP = SOFTMAX_WARP + 4 * QT;
@@ -274,14 +272,13 @@ struct TreeTraits {
   static constexpr int OFF_KV = QT * Q_TILE;
   static constexpr int OFF_STG = OFF_KV + NS * STAGE;
   static constexpr int OFF_SEEN = OFF_STG + 2 * NSTG * STG_TILE;    // [ROWS][8] visible nodes
-  static constexpr int OFF_PAR = OFF_SEEN + ROWS * 32;              // [QT][2][256] parents
-  static constexpr int OFF_ML = OFF_PAR + QT * 2 * PKV_MAX_TREE_NODES * 4;  // group 1's (max, sum)
+  static constexpr int OFF_PAR = OFF_SEEN + ROWS * 32;  // [QT][4 warps][256] parents
+  static constexpr int OFF_ML = OFF_PAR + QT * 4 * PKV_MAX_TREE_NODES * 4;  // group 1's (max, sum)
   static constexpr int OFF_BAR = OFF_ML + (QT - 1) * M * 8;
   static constexpr int B_KFULL = 0, B_KEMPTY = NS, B_VFULL = 2 * NS, B_VEMPTY = 3 * NS;
   static constexpr int B_STG = 4 * NS, B_STGEMPTY = B_STG + 2 * NSTG;
   static constexpr int B_Q = B_STGEMPTY + 2 * NSTG;  // q; per group: o_free, s[2], p[2], o[2]
-  static constexpr int B_GROUP = B_Q + 8 * QT;       // per group: its softmax warps meet
-  static constexpr int B_VREADY = B_GROUP + QT;      // per group: V of its cut tile is in
+  static constexpr int B_VREADY = B_Q + 8 * QT;     // per group: V of its cut tile is in
   static constexpr int B_BOTH = B_VREADY + QT;       // group 1's share of an item
   static constexpr int B_DRAIN = B_BOTH + 1;         // per issuer
   static constexpr int NBAR = B_DRAIN + 2;
@@ -343,7 +340,6 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
     for (int q = 0; q < QT; ++q) {
       mbar_init(bar_q(q), 4);  // one arrival per softmax warp
       mbar_init(bar_ofree(q), 4);
-      mbar_init(bar(Tr::B_GROUP + q), 4);
       mbar_init(bar(Tr::B_VREADY + q), 1);
       for (int b = 0; b < 2; ++b) {
         mbar_init(bar_s(q, b), 1);
@@ -562,7 +558,7 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
     // The whole warp runs the loop and one elected thread issues: with the loop's
     // values the same in all lanes, the descriptors stay in uniform registers,
     // where the MMA wants them.  (One lane alone in the loop moved each of them
-    // there anew: 82 cycles an MMA, now PKV_ISSUE_CYCLES.)
+    // there anew: 557 cycles for the 8 MMAs of an S, now 403.)
     bool ok = true;
     const uint64_t d_q = tc::smem_desc_sw128(sbase, 16, 1024);
     const uint64_t d_k = tc::smem_desc_sw128(sbase + Tr::OFF_KV, 16, 1024);
@@ -681,15 +677,8 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tm = tmem + g * Tr::QCOLS + lanes;
     uint32_t* seen = reinterpret_cast<uint32_t*>(smem + Tr::OFF_SEEN) + (g * M + r) * 8;
-    int* par = reinterpret_cast<int*>(smem + Tr::OFF_PAR) + g * 2 * PKV_MAX_TREE_NODES;
+    int* par = reinterpret_cast<int*>(smem + Tr::OFF_PAR) + (g * 4 + quarter) * PKV_MAX_TREE_NODES;
     float2* s_ml = reinterpret_cast<float2*>(smem + Tr::OFF_ML);
-    int met = 0;
-    // a barrier of the group's warps, bounded as every wait
-    auto group_sync = [&] {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(Tr::B_GROUP + g));
-      return __all_sync(kFullMask, mbar_wait_bounded(bar(Tr::B_GROUP + g), met++ & 1));
-    };
     const int gmask = (1 << p.group_shift) - 1;
     // row `row` of the item's query tile qt in q and out
     auto row_at = [&](const TreeItem& x, int qt, int row) {
@@ -715,12 +704,14 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
         cp_async16(sbase + at, static_cast<const T*>(p.q) + row_at(x, qt, row) * D + ch * 8);
       });
     };
-    auto begin_parents = [&](const TreeItem& x, int parity) {
-      if (!partial(x, x.t1 - 1)) return;
+    // the parents of the nodes up to this warp's last row
+    auto begin_parents = [&](const TreeItem& x) {
       const int qt = in_turn(x) ? 0 : g;
-      const int nodes = ((x.rt * ROWS + qt * M + rows_of(x, qt) - 1) >> p.group_shift) + 1;
-      for (int i = r; i < nodes; i += 128)
-        cp_async4(smem_addr(par + parity * PKV_MAX_TREE_NODES + i), p.parents + x.q0 + i);
+      const int rows = min(rows_of(x, qt), quarter * 32 + 32);
+      if (rows <= quarter * 32 || !partial(x, x.t1 - 1)) return;
+      const int nodes = ((x.rt * ROWS + qt * M + rows - 1) >> p.group_shift) + 1;
+      for (int i = lane; i < nodes; i += 32)
+        cp_async4(smem_addr(par + i), p.parents + x.q0 + i);
     };
     auto end_q = [&](const TreeItem& x, int qt) {
       cp_async_wait_all();
@@ -742,7 +733,7 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
     TreeItem nx;
     bool more = walk.next(p, nx);
     if (more) {
-      begin_parents(nx, 1);
+      begin_parents(nx);
       if (g == 0 || !in_turn(nx)) {
         begin_q(nx, g);
         end_q(nx, g);
@@ -772,34 +763,35 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
             r == 0)
           set_err(p.err, PKV_DEVERR_BAD_SCALE);
       }
-      cp_async_wait_all();  // this thread's share of the parents
+      cp_async_wait_all();  // the parents that this thread loads
+      __syncwarp();
       if (partial(it, it.t1 - 1)) {
         // the nodes that each row sees: itself, its parent, and so on
-        const int node = (it.rt * ROWS + qt * M + min(r, nrows - 1)) >> p.group_shift;
-        const int* up = par + (items & 1) * PKV_MAX_TREE_NODES;
-        ok = group_sync();
-        if (!ok) break;
+        if (active) {
+          const int node = (it.rt * ROWS + qt * M + r) >> p.group_shift;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) seen[w] = 0;
-        int at = node >> 5;
-        uint32_t bits = 0;
-        for (int n = node; n >= 0;) {
-          if ((n >> 5) != at) {
-            seen[at] = bits;
-            at = n >> 5;
-            bits = 0;
+          for (int w = 0; w < 8; ++w) seen[w] = 0;
+          int at = node >> 5;
+          uint32_t bits = 0;
+          for (int n = node; n >= 0;) {
+            if ((n >> 5) != at) {
+              seen[at] = bits;
+              at = n >> 5;
+              bits = 0;
+            }
+            bits |= 1u << (n & 31);
+            const int x = par[n];
+            if (x < -1 || x >= n) {
+              set_err(p.err, PKV_DEVERR_BAD_TREE);
+              break;
+            }
+            n = x;
           }
-          bits |= 1u << (n & 31);
-          const int x = up[n];
-          if (x < -1 || x >= n) {
-            set_err(p.err, PKV_DEVERR_BAD_TREE);
-            break;
-          }
-          n = x;
+          seen[at] = bits;
         }
-        seen[at] = bits;
+        __syncwarp();
         // only an item that ends its unit, and so has tree keys, is followed by another
-        if (more) begin_parents(nx, (items + 1) & 1);
+        if (more) begin_parents(nx);
       }
       // The row's visible keys of tile t, bit by bit.
       auto window = [&](int t) -> unsigned long long {
