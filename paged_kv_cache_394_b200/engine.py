@@ -25,14 +25,21 @@ and copy them on write ([cortexgrid] FAQ on parallel sampling).
 4. fork the samples of a request whose prompt was just prefilled, retire
    sequences that reached their output length, free their pages.
 
-Queries, keys and values are synthetic (seeded N(0,1)): the driver exercises
-the memory manager and the kernels, not a model.  The host work here is
+With a ``drafter`` the running sequences decode speculatively: step 2 reserves a
+slot for every node of the tree that the drafter proposes for a sequence, step 3
+attends with ``paged_attn_tree``, verifies with ``verify_draft`` and moves the
+kept nodes' K/V together with ``compact_accepted``, and step 4 cuts the sequence
+back to what was kept (at least the tree's root, the token sampled last).
+
+Queries, keys and values are synthetic (seeded N(0,1)), and so are a drafted
+step's probabilities and uniforms: the driver exercises the memory manager and
+the kernels, not a model.  The host work here is
 orchestration; allocation is the C++ allocator and every tensor operation is
 a CUDA kernel of libpagedkv.
 """
 
 from collections import deque
-from dataclasses import dataclass
+from dataclasses import dataclass, field
 
 import numpy as np
 import torch
@@ -65,12 +72,19 @@ class StepRecord:
     used_blocks: int
     cached_tokens: int
     kernel_ms: float
+    parents: list = field(default_factory=list)  # the tree of each decoded sequence (drafted steps)
+    kept: list = field(default_factory=list)     # how many of its nodes were kept
+    next_tokens: list = field(default_factory=list)
 
 
 class ContinuousBatcher:
     def __init__(self, num_blocks, block_size, num_heads, num_kv_heads, head_dim,
                  dtype=torch.float16, max_num_seqs=256, max_num_batched_tokens=2048,
-                 max_model_len=4096, seed=0, device="cuda", free_order=None, values=None):
+                 max_model_len=4096, seed=0, device="cuda", free_order=None, values=None,
+                 drafter=None, max_draft=16, vocab_size=32000, draws=None):
+        """``drafter(seq_id, context_len)`` returns the parents of a tree of at most
+        ``max_draft`` nodes, its root (the token sampled last) first, as
+        paged_attn_tree takes them; None decodes one token a step."""
         self.bs = block_size
         self.h, self.hkv, self.d = num_heads, num_kv_heads, head_dim
         self.dtype = dtype
@@ -86,16 +100,26 @@ class ContinuousBatcher:
         self.gen = torch.Generator(device=self.device)
         self.gen.manual_seed(seed)
         # values(kind, shape) -> device tensor of self.dtype, kind in
-        # {"key", "value", "q_prefill", "q_decode"}; N(0,1) from the device RNG by default
+        # {"key", "value", "q_prefill", "q_decode", "q_tree"}; N(0,1) from the device RNG by
+        # default
         self.values = values or (lambda kind, shape: torch.randn(
             *shape, generator=self.gen, device=self.device, dtype=torch.float32).to(self.dtype))
+        if drafter is not None and not 1 <= max_draft <= pk.MAX_TREE_NODES:
+            raise ValueError("max_draft must be 1 .. %d" % pk.MAX_TREE_NODES)
+        self.drafter, self.max_draft, self.vocab = drafter, max_draft, vocab_size
+        # draws(parents, query_start) -> the model's and the draft's part of a drafted
+        # step: (target_probs [T, V], draft_probs [T, V] or None, draft_tokens [T],
+        # accept_uniforms [T], sample_uniforms [S]), synthetic by default
+        self.draws = draws or self._synthetic_draws
+        # blocks a running sequence may take in one step
+        self.step_blocks = 1 if drafter is None else 1 + -(-max_draft // block_size)
         self.waiting = deque()
         self.running = {}       # seq id -> remaining tokens to generate
         self.next_seq = 0
         self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.scale = 1.0 / float(np.sqrt(head_dim))
         self.step_index = 0
-        self.last_outputs = {}  # "prefill" / "decode" -> output tensors of the last step
+        self.last_outputs = {}  # "prefill" / "decode" / "tree" -> output tensors of the last step
 
     # -- request queue -----------------------------------------------------
     def submit(self, req):
@@ -108,7 +132,7 @@ class ContinuousBatcher:
         alloc = self.alloc
         # 1. admission, in arrival order
         admitted = []
-        budget = self.max_batched - len(self.running)
+        budget = self.max_batched - len(self.running) * (self.max_draft if self.drafter else 1)
         while self.waiting:
             req = self.waiting[0]
             if req.arrival > self.step_index:
@@ -117,9 +141,10 @@ class ContinuousBatcher:
                 break
             if req.prompt_len > budget:
                 break
-            # keep one free block per running sequence for this step's appends
+            # keep the blocks that the running sequences may take in this step
             need = -(-req.prompt_len // self.bs)
-            if alloc.num_free() < need + len(self.running) + len(admitted) * req.samples:
+            if alloc.num_free() < need + (len(self.running) * self.step_blocks
+                                          + len(admitted) * req.samples):
                 break
             sid = self.next_seq
             try:
@@ -132,12 +157,18 @@ class ContinuousBatcher:
             self.next_seq += 1
             budget -= req.prompt_len
             admitted.append((sid, req))
-        # 2. one new slot per running sequence (CoW pairs for shared partial blocks)
+        # 2. one new slot per running sequence, or per node of its tree (CoW pairs for
+        #    shared partial blocks)
         decoded = list(self.running)
-        slots_dec, pairs = [], []
+        slots_dec, pairs, trees = [], [], []
         if decoded:
+            owners = decoded
+            if self.drafter is not None:
+                hist = alloc.context_lens(decoded)
+                trees = [self._tree(sid, n) for sid, n in zip(decoded, hist)]
+                owners = [sid for sid, t in zip(decoded, trees) for _ in t]
             try:
-                slots_dec, pairs = alloc.append_slots(decoded)
+                slots_dec, pairs = alloc.append_slots(owners)
             except pk.PagedKVError as e:
                 if e.status != pk.ERR_OUT_OF_BLOCKS:
                     raise
@@ -168,10 +199,20 @@ class ContinuousBatcher:
                                     dtype=torch.int32, device=self.device)
             ctx_list = alloc.context_lens(decoded)
             d_ctx = torch.tensor(ctx_list, dtype=torch.int32, device=self.device)
-            # one CTA per partition that exists, planned from the host's lengths
-            d_part = pk.partition_size(n_dec, self.hkv, self.bs, max(ctx_list))
-            d_work = pk.decode_plan(ctx_list, self.bs, d_part).to(self.device)
-            d_q = self.values("q_decode", (n_dec, self.h, self.d))
+            if trees:
+                n_max = max(len(t) for t in trees)
+                d_qs = torch.tensor(np.concatenate([[0], np.cumsum([len(t) for t in trees])]),
+                                    dtype=torch.int32, device=self.device)
+                d_par = torch.tensor(sum(trees, []), dtype=torch.int32, device=self.device)
+                probs, q_probs, tokens, u, u_next = self.draws(d_par, d_qs)
+                accepted = torch.empty((len(trees), n_max), dtype=torch.int32, device=self.device)
+                kept = torch.empty(len(trees), dtype=torch.int32, device=self.device)
+                sampled = torch.empty_like(kept)
+            else:
+                # one CTA per partition that exists, planned from the host's lengths
+                d_part = pk.partition_size(n_dec, self.hkv, self.bs, max(ctx_list))
+                d_work = pk.decode_plan(ctx_list, self.bs, d_part).to(self.device)
+            d_q = self.values("q_tree" if trees else "q_decode", (n_dec, self.h, self.d))
             d_out = torch.empty_like(d_q)
         pair_t = torch.tensor(pairs, dtype=torch.int64, device=self.device) if pairs else None
         t0 = torch.cuda.Event(enable_timing=True)
@@ -187,7 +228,16 @@ class ContinuousBatcher:
                                   self.scale, self.hkv, self.bs, max(lens), max(lens),
                                   dev_err=self.err)
             self.last_outputs["prefill"] = (ids, p_q, p_out, p_tables, p_ctx, p_qs)
-        if decoded:
+        if trees:
+            pk.paged_attn_tree(d_out, d_q, self.k_cache, self.v_cache, d_tables, d_ctx, d_qs,
+                               d_par, self.scale, self.hkv, self.bs, max(ctx_list), n_max,
+                               dev_err=self.err)
+            pk.verify_draft(accepted, kept, sampled, probs, tokens, d_par, d_qs, u, u_next, n_max,
+                            draft_probs=q_probs, dev_err=self.err)
+            pk.compact_accepted(self.k_cache, self.v_cache, d_tables, d_ctx, d_qs, accepted, kept,
+                                dev_err=self.err)
+            self.last_outputs["tree"] = (decoded, d_q, d_out, d_tables, d_ctx, d_qs, accepted)
+        elif decoded:
             pk.paged_attn_decode(d_out, d_q, self.k_cache, self.v_cache, d_tables, d_ctx,
                                  self.scale, self.hkv, self.bs, max(ctx_list),
                                  partition_size=d_part, dev_err=self.err, work=d_work)
@@ -200,9 +250,12 @@ class ContinuousBatcher:
             raise RuntimeError("device error word %d" % int(self.err.item()))
         # 4. bookkeeping: samples fork after their prompt, finished sequences free pages
         finished = []
-        for sid in decoded:
-            self.running[sid] -= 1
-            if self.running[sid] == 0:
+        n_kept = kept.tolist() if trees else [1] * len(decoded)
+        for i, sid in enumerate(decoded):
+            if trees:
+                alloc.truncate(sid, hist[i] + n_kept[i])
+            self.running[sid] -= n_kept[i]
+            if self.running[sid] <= 0:
                 del self.running[sid]
                 alloc.free_seq(sid)
                 finished.append(sid)
@@ -222,10 +275,44 @@ class ContinuousBatcher:
                           forked=forked,
                           new_tokens=n_pre + n_dec, prefill_tokens=n_pre, finished=finished,
                           live=len(self.running), waiting=len(self.waiting), used_blocks=used,
-                          cached_tokens=cached, kernel_ms=t0.elapsed_time(t1))
+                          cached_tokens=cached, kernel_ms=t0.elapsed_time(t1), parents=trees,
+                          kept=n_kept if trees else [],
+                          next_tokens=sampled.tolist() if trees else [])
+
+    # -- drafts ------------------------------------------------------------------
+    def _tree(self, sid, context_len):
+        """The sequence's tree, cut to what max_model_len leaves room for."""
+        parents = [int(x) for x in self.drafter(sid, context_len)]
+        if not 1 <= len(parents) <= self.max_draft:
+            raise ValueError("a tree must have 1 .. max_draft nodes")
+        if parents[0] != -1 or any(not 0 <= x < j for j, x in enumerate(parents) if j):
+            raise ValueError("a tree has one root, and parents before their nodes")
+        return parents[:self.max_model_len - context_len]
+
+    def _synthetic_draws(self, parents, query_start):
+        t, v = parents.numel(), self.vocab
+        rand = lambda *n: torch.rand(*n, generator=self.gen, device=self.device)  # noqa: E731
+        logits = 4.0 * torch.randn((t, v), generator=self.gen, device=self.device)
+        noise = torch.randn((t, v), generator=self.gen, device=self.device)
+        target, draft = torch.softmax(logits, 1), torch.softmax(logits + 0.8 * noise, 1)
+        # a node's token is drawn from the draft's distribution at its parent
+        starts = torch.repeat_interleave(query_start[:-1], query_start[1:] - query_start[:-1])
+        rows = (starts + parents.clamp(min=0)).long()
+        c = torch.cumsum(draft[rows], dim=1)
+        tokens = torch.searchsorted(c, rand(t, 1) * c[:, -1:])[:, 0].clamp(max=v - 1)
+        return target, draft, tokens.int(), rand(t), rand(query_start.numel() - 1)
 
     def idle(self):
         return not self.waiting and not self.running
+
+
+def tree_drafter(seed, nodes):
+    """A drafter of random trees of 1 .. nodes nodes."""
+    rng = np.random.default_rng(seed)
+
+    def draft(sid, context_len):
+        return [-1] + [int(j * rng.random() ** 1.5) for j in range(1, rng.integers(1, nodes + 1))]
+    return draft
 
 
 def synthetic_trace(seed, num_requests, mean_interarrival=0.5, prompt_median=300,
