@@ -40,6 +40,44 @@ def test_every_e4m3_shape(pk, d, bs, g, dtype):
     t.check()
 
 
+def some_rows(w, count, seed=0):
+    """Rows at random, and each sequence's first and last."""
+    rng = np.random.default_rng(seed)
+    total, h = len(w.q), w.num_heads
+    rows = {(int(a), int(b)) for a, b in zip(rng.integers(0, total, count),
+                                             rng.integers(0, h, count))}
+    for a, b in zip(w.query_start[:-1], w.query_start[1:]):
+        if b > a:
+            rows |= {(int(a), 0), (int(b) - 1, h - 1)}
+    return rows
+
+
+# units cut into several pieces, of one and of two query tiles, beside short ones
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d,bs,g,dtype", SHAPES)
+def test_every_shape_in_pieces(pk, d, bs, g, dtype, fp8):
+    w = tree_workload([1700, 33, 64, 900, 0], [21, 0, 40, 3, 64], 2 * g, 2, d, bs, dtype,
+                      seed=3 * d + bs + g)
+    t = TreeOnDevice(pk, w, scales=([0.0125, 0.02], [0.01, 0.03]) if fp8 else None)
+    assert t.run() == 0
+    t.check(some_rows(w, 20))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_many_sequences(pk, fp8):
+    """More sequences than a CTA has threads, most of one tile, some empty, one
+    long (cut) or none (more units than CTAs, left whole)."""
+    rng = np.random.default_rng(5)
+    for extra in ([3000], []):
+        hist = extra + [int(x) for x in rng.integers(0, 60, 700)]
+        nodes = [int(x) for x in rng.integers(0, 5, len(hist))]
+        nodes[0] = 7
+        w = tree_workload(hist, nodes, 2, 1, 64, 16, "fp16", seed=41)
+        t = TreeOnDevice(pk, w, scales=([0.0125], [0.01]) if fp8 else None)
+        assert t.run() == 0
+        t.check()
+
+
 @pytest.mark.parametrize("kind", ["chain", "star", "forest"])
 @pytest.mark.parametrize("g,dtype", [(1, "fp16"), (8, "bf16")])
 def test_largest_trees_of_each_kind(pk, kind, g, dtype):
@@ -95,11 +133,13 @@ def test_chain_is_prefill_and_one_node_is_decode(pk):
         close(widen_out(dev_to_bits(o), w), ref, mag, "bf16")
 
 
+@pytest.mark.parametrize("hist,heads", [([70, 20], 8), ([1130, 20], 8), ([1130, 650], 2),
+                                        ([70, 20], 2)])
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("d,dtype", [(128, "bf16"), (128, "fp16"), (64, "fp16")])
-def test_what_a_row_does_not_see_does_not_enter_it(pk, d, dtype, fp8):
+def test_what_a_row_does_not_see_does_not_enter_it(pk, d, dtype, fp8, hist, heads):
     """NaN and infinities in a node's K and V reach its descendants only."""
-    w = tree_workload([70, 20], [40, 24], 8, 2, d, 16, dtype, seed=11)
+    w = tree_workload(hist, [40, 24], heads, 2, d, 16, dtype, seed=11)
     t = TreeOnDevice(pk, w, scales=([0.0125, 0.02], [0.01, 0.03]) if fp8 else None)
     ref, mag = t.reference()
     inf, nan = ((0x7C00, 0x7E00) if dtype == "fp16" else (0x7F80, 0x7FC0)) if not fp8 else (
