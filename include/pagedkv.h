@@ -615,7 +615,8 @@ pkv_status pkv_paged_attn_decode_cascade_fp8(
  *
  *   workspace     device scratch, 16-byte aligned, of at least
  *                 pkv_paged_attn_tree_workspace_bytes(...) bytes for the same
- *                 shape (less, or none: PKV_ERR_WORKSPACE).  It needs no
+ *                 shape (less, or none: PKV_ERR_WORKSPACE; where that is 0, as
+ *                 for short contexts, it may be NULL).  It needs no
  *                 preparation and holds nothing afterwards; calls that may run
  *                 at the same time need one each.
  *

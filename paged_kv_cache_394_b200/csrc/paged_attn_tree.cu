@@ -73,7 +73,8 @@ int tree_ctas(int resident, int rows, int num_seqs, int group, int num_kv_heads,
   return static_cast<int>(std::min<long long>(resident, most));
 }
 
-size_t tree_ws_bytes(int ctas, int rows, int head_dim) {
+size_t tree_ws_bytes(int ctas, int rows, int head_dim, bool whole) {
+  if (whole) return 0;
   return static_cast<size_t>(ctas) *
          (sizeof(int4) + 2 * static_cast<size_t>(rows) * (8 + 4 * static_cast<size_t>(head_dim)));
 }
@@ -112,7 +113,11 @@ pkv_status tree_launch(void* out, const void* q, const void* k_cache, const void
   const TreeEntry e = tree_entry(head_dim, dtype, fp8, max_rows);
   const int ctas = tree_ctas(e.ctas, e.rows, num_seqs, group, num_kv_heads, max_context_len,
                              max_query_len);
-  if (!workspace || !aligned16(workspace) || workspace_bytes < tree_ws_bytes(ctas, e.rows, head_dim))
+  const int max_rts = (max_rows + e.rows - 1) / e.rows;
+  const long long units = static_cast<long long>(num_seqs) * max_rts * num_kv_heads;
+  const bool whole = tree_whole(units, max_context_len);
+  const size_t need = tree_ws_bytes(ctas, e.rows, head_dim, whole);
+  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need))
     return PKV_ERR_WORKSPACE;
   const pkv_dtype cdt = fp8 ? PKV_FP8_E4M3 : dtype;
   CUtensorMap kmap, vmap;
@@ -143,14 +148,15 @@ pkv_status tree_launch(void* out, const void* q, const void* k_cache, const void
   p.max_context_len = max_context_len;
   p.max_query_len = max_query_len;
   p.num_blocks = num_blocks;
-  p.max_rts = (max_rows + e.rows - 1) / e.rows;
-  const long long units = static_cast<long long>(num_seqs) * p.max_rts * num_kv_heads;
-  p.whole_units = tree_whole(units, max_context_len);
-  p.direct = p.whole_units && units == ctas;
+  p.max_rts = max_rts;
+  p.whole_units = whole;
+  p.direct = whole && units == ctas;
   p.err = dev_err;
-  p.ws_meta = static_cast<int4*>(workspace);
-  p.ws_o = reinterpret_cast<float*>(p.ws_meta + ctas);
-  p.ws_ml = reinterpret_cast<float2*>(p.ws_o + static_cast<size_t>(ctas) * 2 * e.rows * head_dim);
+  if (!whole) {
+    p.ws_meta = static_cast<int4*>(workspace);
+    p.ws_o = reinterpret_cast<float*>(p.ws_meta + ctas);
+    p.ws_ml = reinterpret_cast<float2*>(p.ws_o + static_cast<size_t>(ctas) * 2 * e.rows * head_dim);
+  }
   st = cuda_status(cudaFuncSetAttribute(e.fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         static_cast<int>(e.smem)));
   if (st != PKV_OK) return st;
@@ -181,7 +187,10 @@ extern "C" size_t pkv_paged_attn_tree_workspace_bytes(int num_seqs, int num_head
     const TreeEntry e = tree_entry(head_dim, PKV_FP16, fp8, max_query_len * group);
     const int ctas = tree_ctas(e.ctas, e.rows, num_seqs, group, num_kv_heads, max_context_len,
                                max_query_len);
-    most = std::max(most, tree_ws_bytes(ctas, e.rows, head_dim));
+    const long long rts = (max_query_len * group + e.rows - 1) / e.rows;
+    most = std::max(most, tree_ws_bytes(ctas, e.rows, head_dim,
+                                        tree_whole(num_seqs * rts * num_kv_heads,
+                                                   max_context_len)));
   }
   return most;
 }

@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
         at -= w;
       }
     }
-    if (threadIdx.x == 0) p.ws_meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (threadIdx.x == 0 && !p.whole_units) p.ws_meta[blockIdx.x] = make_int4(0, 0, 0, 0);
     tc::tc_fence_before();
     __syncthreads();
     walk.seq = s_found[0];

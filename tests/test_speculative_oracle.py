@@ -282,10 +282,11 @@ def test_tree_refusals(pk, fp8):
         assert tree_call(pk, fp8, **over) == uns, over
     for over in (dict(num_seqs=0), dict(num_tokens=0), dict(mq=0)):
         assert tree_call(pk, fp8, **over) == pk.OK, over
-    need = pk.tree_workspace_bytes(2, 8, 2, 128, 100, 4)
-    assert need > 0
+    long = dict(mctx=6000, mb=400)    # short contexts need no workspace
+    assert pk.tree_workspace_bytes(2, 8, 2, 128, 100, 4) == 0
+    assert pk.tree_workspace_bytes(2, 8, 2, 128, 6000, 4) > 0
     for over in (dict(ws=None), dict(ws=BAD), dict(ws_bytes=0), dict(ws_bytes=16)):
-        assert tree_call(pk, fp8, **over) == pk.ERR_WORKSPACE, over
+        assert tree_call(pk, fp8, **over, **long) == pk.ERR_WORKSPACE, over
     if fp8:
         assert tree_call(pk, True, ks=None) == inv and tree_call(pk, True, vs=None) == inv
 
