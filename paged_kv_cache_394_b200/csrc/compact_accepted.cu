@@ -128,7 +128,9 @@ extern "C" pkv_status pkv_compact_accepted(void* k_cache, void* v_cache,
   if (!k_cache || !v_cache || !block_tables || !context_lens || !query_start || !accepted ||
       !num_accepted)
     return PKV_ERR_INVALID_ARG;
-  if (!aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_INVALID_ARG;
+  if (!aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned4(block_tables, context_lens, query_start, accepted, num_accepted, dev_err))
+    return PKV_ERR_INVALID_ARG;
   const int chunks = head_dim * cache_elem_bytes(dtype) / 16;
   const int64_t slices = (static_cast<int64_t>(num_kv_heads) * chunks + 255) / 256;
   if (slices > 65535) return PKV_ERR_UNSUPPORTED;

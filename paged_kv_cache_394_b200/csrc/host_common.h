@@ -16,6 +16,12 @@ pkv_status cuda_status(cudaError_t e);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Every pointer (null counts) on a 4-byte boundary.
+template <class... P>
+inline bool aligned4(const P*... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ...) & 3u) == 0;
+}
+
 inline bool head_dim_supported(int d) { return d == 64 || d == 128; }
 inline bool block_size_supported(int bs) { return bs == 16 || bs == 32; }
 inline bool dtype_valid(int dt) { return dt == PKV_FP16 || dt == PKV_BF16; }

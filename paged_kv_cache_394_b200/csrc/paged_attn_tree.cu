@@ -107,7 +107,8 @@ pkv_status tree_launch(void* out, const void* q, const void* k_cache, const void
   if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start ||
       !parents)
     return PKV_ERR_INVALID_ARG;
-  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned4(block_tables, context_lens, query_start, parents, k_scales, v_scales, dev_err))
     return PKV_ERR_INVALID_ARG;
   const int max_rows = max_query_len * group;
   const TreeEntry e = tree_entry(head_dim, dtype, fp8, max_rows);

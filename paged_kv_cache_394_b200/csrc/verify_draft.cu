@@ -493,6 +493,9 @@ extern "C" pkv_status pkv_verify_draft(
       (num_tokens > 0 && (!target_probs || !draft_tokens || !parents || !accept_uniforms)) ||
       !sample_uniforms)
     return PKV_ERR_INVALID_ARG;
+  if (!aligned4(accepted, num_accepted, next_token, draft_tokens, parents, query_start,
+                accept_uniforms, sample_uniforms, dev_err))
+    return PKV_ERR_INVALID_ARG;
   const uintptr_t mask = f32 ? 3u : 1u;
   if ((reinterpret_cast<uintptr_t>(target_probs) & mask) ||
       (reinterpret_cast<uintptr_t>(draft_probs) & mask))

@@ -252,7 +252,7 @@ def test_truncate_refusals_and_cached_blocks(pk):
 
 
 # ---- host checks of the C ABI -------------------------------------------------
-GOOD, BAD = ctypes.c_void_p(0x1000), ctypes.c_void_p(0x1008)
+GOOD, BAD, ODD = ctypes.c_void_p(0x1000), ctypes.c_void_p(0x1008), ctypes.c_void_p(0x1002)
 
 
 def tree_call(pk, fp8=False, **over):
@@ -272,6 +272,8 @@ def test_tree_refusals(pk, fp8):
         assert tree_call(pk, fp8, **{name: None}) == inv, name
     for name in ("out", "q", "k", "v"):
         assert tree_call(pk, fp8, **{name: BAD}) == inv, name
+    for name in ("tables", "lens", "qs", "parents", "err") + (("ks", "vs") if fp8 else ()):
+        assert tree_call(pk, fp8, **{name: ODD}) == inv, name
     for over in (dict(num_seqs=-1), dict(num_tokens=-1), dict(heads=0), dict(kv=0), dict(mb=0),
                  dict(mctx=-1), dict(mq=-1), dict(nb=0), dict(dt=2), dict(dt=3), dict(dt=9),
                  dict(heads=7), dict(scale=float("nan")), dict(scale=float("inf")), dict(mq=101),
@@ -303,6 +305,8 @@ def test_verify_refusals(pk):
     inv, uns = pk.ERR_INVALID_ARG, pk.ERR_UNSUPPORTED
     for name in ("acc", "cnt", "nxt", "p", "tok", "par", "qs", "u", "un"):
         assert verify_call(pk, **{name: None}) == inv, name
+    for name in ("acc", "cnt", "nxt", "p", "q", "tok", "par", "qs", "u", "un", "err"):
+        assert verify_call(pk, **{name: ODD}) == inv, name
     for over in (dict(num_seqs=-1), dict(num_tokens=-1), dict(mq=-1), dict(vocab=0), dict(dt=2),
                  dict(dt=4), dict(ps=99), dict(qstr=99), dict(p=ctypes.c_void_p(0x1002)),
                  dict(q=ctypes.c_void_p(0x1002)), dict(dt=0, p=ctypes.c_void_p(0x1001))):
@@ -323,6 +327,8 @@ def test_compact_refusals(pk):
     inv, uns = pk.ERR_INVALID_ARG, pk.ERR_UNSUPPORTED
     for name in ("k", "v", "tables", "lens", "qs", "acc", "cnt"):
         assert compact_call(pk, **{name: None}) == inv, name
+    for name in ("tables", "lens", "qs", "acc", "cnt", "err"):
+        assert compact_call(pk, **{name: ODD}) == inv, name
     for over in (dict(k=BAD), dict(v=BAD), dict(num_seqs=-1), dict(mq=-1), dict(kv=0), dict(mb=0),
                  dict(nb=0), dict(dt=3), dict(dt=-1)):
         assert compact_call(pk, **over) == inv, over
