@@ -16,17 +16,19 @@ using TreeMergeFn = void (*)(const TreeParams);
 
 struct TreeEntry {
   TreeFn fn;
-  TreeMergeFn merge;
+  TreeMergeFn merge, merge_many;  // for few and for many pieces a unit
   size_t smem;
   int threads, rows, ctas;  // ctas: those resident at once
 };
 
 constexpr int kSms = 148;
+constexpr int kMergeSlices = 4;
 
 template <int D, class DT, bool FP8, int QT>
 TreeEntry tree_entry() {
   using Tr = TreeTraits<D, DT, FP8, QT>;
-  return {paged_attn_tree_kernel<Tr>, paged_attn_tree_merge_kernel<D, Tr::ROWS, DT>,
+  return {paged_attn_tree_kernel<Tr>, paged_attn_tree_merge_kernel<D, Tr::ROWS, DT, 1>,
+          paged_attn_tree_merge_kernel<D, Tr::ROWS, DT, kMergeSlices>,
           Tr::smem_bytes(), Tr::THREADS, Tr::ROWS, kSms * Tr::MIN_BLOCKS};
 }
 
@@ -152,6 +154,9 @@ pkv_status tree_launch(void* out, const void* q, const void* k_cache, const void
   p.max_rts = max_rts;
   p.whole_units = whole;
   p.direct = whole && units == ctas;
+  const bool many = units * 2 * kMergeSlices <= ctas;
+  p.by_unit = many;
+  p.num_ctas = ctas;
   p.err = dev_err;
   if (!whole) {
     p.ws_meta = static_cast<int4*>(workspace);
@@ -164,10 +169,17 @@ pkv_status tree_launch(void* out, const void* q, const void* k_cache, const void
   st = cuda_status(launch_after_previous_smem(e.fn, dim3(ctas), dim3(e.threads), e.smem, stream, p,
                                               kmap, vmap));
   if (st != PKV_OK || ctas == 1 || p.whole_units) return st;
+  // Units in eight or more pieces on average are joined by slices of threads, from
+  // entries by unit: one sequence of 32000 tokens takes 41.8 us so, 50.1 by one set
+  // of threads and entries by CTA, which suit the batches in two or three pieces a
+  // unit (GQA chat 72 against 76 us, 8 sequences of 1200 tokens 19.8 against 25.3).
+  const int entries = p.by_unit ? static_cast<int>(units) : ctas;
+  const int rows = kTreeMergeThreads / (head_dim / 4) / (many ? kMergeSlices : 1);
   // at most about as many blocks as are resident at once
-  const dim3 merge(ctas, std::min((std::min(max_rows, e.rows) + 7) / 8, 2400 / ctas));
-  return cuda_status(
-      launch_after_previous(e.merge, merge, dim3(8 * head_dim / 4), stream, p));
+  const dim3 merge(entries, std::min((std::min(max_rows, e.rows) + rows - 1) / rows,
+                                     std::max(1, 2400 / entries)));
+  return cuda_status(launch_after_previous(many ? e.merge_many : e.merge, merge,
+                                           dim3(kTreeMergeThreads), stream, p));
 }
 
 }  // namespace

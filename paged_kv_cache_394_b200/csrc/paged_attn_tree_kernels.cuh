@@ -73,10 +73,14 @@ struct TreeParams {
   int block_size, max_blocks_per_seq, max_context_len, max_query_len, num_blocks;
   int whole_units;  // units are not cut
   int direct;       // ... and each has its CTA: max_rts for every (sequence, kv head)
-  int max_rts;
+  int max_rts, num_ctas;
   unsigned* err;
-  // Workspace: for each CTA one merge entry {first token, kv head, first CTA,
-  // rows} (rows = 0: nothing to merge) and two pieces of ROWS rows.
+  // Workspace: for each CTA one merge entry and two pieces of ROWS rows.  Entry c
+  // is of the unit that ended in CTA c, {first token, kv head, first CTA, rows},
+  // rows = 0 where none did that another CTA began; or, with no more units than
+  // CTAs (by_unit), entry u is of unit u (of max_rts for every (sequence, kv head)),
+  // {first CTA, last CTA}, the same one where the unit is not cut.
+  int by_unit;
   int4* ws_meta;
   float2* ws_ml;  // (max, sum) of each row of each piece
   float* ws_o;    // [pieces][D / 4][ROWS][4]
@@ -442,7 +446,8 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
         at -= w;
       }
     }
-    if (threadIdx.x == 0 && !p.whole_units) p.ws_meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (threadIdx.x == 0 && !p.whole_units && !p.by_unit)
+      p.ws_meta[blockIdx.x] = make_int4(0, 0, 0, 0);
     tc::tc_fence_before();
     __syncthreads();
     walk.seq = s_found[0];
@@ -1110,14 +1115,17 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
         mbar_arrive(bar_ofree(g));
         if (both) mbar_arrive(bar_ofree(1));
       }
-      if (g == 0 && r == 0 && it.t0 > 0 && it.t1 == it.nt) {
-        // this CTA ends a unit that another began: the one whose stretch holds
-        // the unit's first tile, `lead` positions before this stretch's start
-        const int before = (it.lead + len - 1) / len;
-        p.ws_meta[blockIdx.x] =
-            make_int4(it.q0 + ((it.rt * ROWS) >> p.group_shift), it.kvh,
-                      static_cast<int>(blockIdx.x) - before,
-                      min(ROWS, (it.q_len << p.group_shift) - it.rt * ROWS));
+      if (g == 0 && r == 0 && it.t1 == it.nt && !p.whole_units) {
+        // this CTA ends the unit; the one whose stretch holds the unit's first tile,
+        // `lead` positions before this stretch's start, began it
+        const int began = static_cast<int>(blockIdx.x) - (it.t0 > 0 ? (it.lead + len - 1) / len : 0);
+        if (p.by_unit)
+          p.ws_meta[(it.seq * p.num_kv_heads + it.kvh) * p.max_rts + it.rt] =
+              make_int4(began, blockIdx.x, 0, 0);
+        else if (it.t0 > 0)
+          p.ws_meta[blockIdx.x] =
+              make_int4(it.q0 + ((it.rt * ROWS) >> p.group_shift), it.kvh, began,
+                        min(ROWS, (it.q_len << p.group_shift) - it.rt * ROWS));
       }
     }
     if (!ok && lane == 0) set_err(p.err, PKV_DEVERR_TIMEOUT);
@@ -1204,48 +1212,85 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
 
 // Joins the pieces of the units that lie across CTAs' stretches: with M = max m,
 //   out = sum 2^(m - M) o / sum 2^(m - M) l.
-// Entry blockIdx.x is of the unit that ended in that CTA; the piece of the unit's
-// first CTA is that CTA's second, of every later one its first.  A thread has 4
-// dims of a row, a warp 2 rows x 64 dims (whole sectors of the pieces), a block
-// 8 rows, blockIdx.y of them first and every gridDim.y-th; 8 pieces' loads are
-// under way at once.
-template <int D, int ROWS, class DT>
-__global__ void __launch_bounds__(8 * D / 4) paged_attn_tree_merge_kernel(const TreeParams p) {
+// The piece of a unit's first CTA is that CTA's second, of every later one its
+// first.  A thread has 4 dims of a row, a warp 2 rows x 64 dims (whole sectors of
+// the pieces), and SLICES sets of threads take every SLICES-th piece and meet in
+// shared memory.  Block (i, j) takes entry i, of its groups of rows the j-th and
+// every gridDim.y-th after.  It is bound by the latency of its loads: N of them
+// are under way at once, 8 for units in many pieces, 3 where a unit has two or
+// three, which leaves 8 blocks an SM (GQA chat batch 72.9 us with 8, 68.4 with 3).
+constexpr int kTreeMergeThreads = 256;
+template <int D, int ROWS, class DT, int SLICES>
+__global__ void __launch_bounds__(kTreeMergeThreads, SLICES > 1 ? 1 : 8)
+    paged_attn_tree_merge_kernel(const TreeParams p) {
   using T = typename DT::T;
+  constexpr int PER = kTreeMergeThreads / SLICES;  // threads of a slice
+  constexpr int RB = PER / (D / 4);                // rows of a block
+  constexpr int N = SLICES > 1 ? 8 : 3;
+  static_assert(RB % 2 == 0, "a warp takes two rows");
+  __shared__ float part[SLICES > 1 ? SLICES : 1][6][SLICES > 1 ? PER : 1];
   grid_dependency_wait();
   trigger_dependents();
-  const int4 e = p.ws_meta[blockIdx.x];
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int4 e = p.ws_meta[blockIdx.x];
+  const int slice = threadIdx.x / PER, t = threadIdx.x % PER;
+  const int w = t >> 5, lane = t & 31;
   const int c4 = (w % (D / 64)) * 16 + (lane >> 1);
-  const int last = static_cast<int>(blockIdx.x);
-  for (int r = static_cast<int>(blockIdx.y) * 8 + (w / (D / 64)) * 2 + (lane & 1); r < e.w;
-       r += 8 * gridDim.y) {
+  int last = static_cast<int>(blockIdx.x);
+  if (p.by_unit) {
+    const int seq = static_cast<int>(blockIdx.x) / (p.num_kv_heads * p.max_rts);
+    const int rt = static_cast<int>(blockIdx.x) % p.max_rts;
+    TreeSeq s;
+    if (!tree_seq(p, tree_lens(p, seq), s, false)) return;
+    last = e.y;
+    // only what a CTA that gave up left unwritten is out of range
+    if (e.x < 0 || e.x >= last || last >= p.num_ctas) return;
+    e = make_int4(s.q0 + ((rt * ROWS) >> p.group_shift),
+                  static_cast<int>(blockIdx.x) / p.max_rts % p.num_kv_heads, e.x,
+                  min(ROWS, (s.q_len << p.group_shift) - rt * ROWS));
+  }
+  for (int r0 = static_cast<int>(blockIdx.y) * RB; r0 < e.w; r0 += RB * gridDim.y) {
+    const int r = r0 + (w / (D / 64)) * 2 + (lane & 1);
     float big = -INFINITY, num[4] = {}, den = 0.f;
-    constexpr int N = 8;
-    for (int c0 = e.z; c0 <= last; c0 += N) {
-      float2 ml[N];
-      float4 o[N];
+    auto add = [&](float m1, float l1, const float4& o) {
+      const float m = m1 == -INFINITY ? big : fmaxf(big, m1);
+      const float a = big == -INFINITY ? 0.f : exp2_approx(big - m);
+      const float f = m1 == -INFINITY ? 0.f : exp2_approx(m1 - m);
+      big = m;
+      den = den * a + f * l1;
+      num[0] = num[0] * a + f * o.x;
+      num[1] = num[1] * a + f * o.y;
+      num[2] = num[2] * a + f * o.z;
+      num[3] = num[3] * a + f * o.w;
+    };
+    if (r < e.w) {
+      for (int c0 = e.z + slice; c0 <= last; c0 += N * SLICES) {
+        float2 ml[N];
+        float4 o[N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int c = min(c0 + i, last);
-        const size_t piece = static_cast<size_t>(c) * 2 + (c == e.z ? 1 : 0);
-        ml[i] = p.ws_ml[piece * ROWS + r];
-        o[i] = reinterpret_cast<const float4*>(p.ws_o)[(piece * (D / 4) + c4) * ROWS + r];
-      }
+        for (int i = 0; i < N; ++i) {
+          const int c = min(c0 + i * SLICES, last);
+          const size_t piece = static_cast<size_t>(c) * 2 + (c == e.z ? 1 : 0);
+          ml[i] = p.ws_ml[piece * ROWS + r];
+          o[i] = reinterpret_cast<const float4*>(p.ws_o)[(piece * (D / 4) + c4) * ROWS + r];
+        }
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (c0 + i > last) break;
-        const float m = ml[i].x == -INFINITY ? big : fmaxf(big, ml[i].x);
-        const float a = big == -INFINITY ? 0.f : exp2_approx(big - m);
-        const float f = ml[i].x == -INFINITY ? 0.f : exp2_approx(ml[i].x - m);
-        big = m;
-        den = den * a + f * ml[i].y;
-        num[0] = num[0] * a + f * o[i].x;
-        num[1] = num[1] * a + f * o[i].y;
-        num[2] = num[2] * a + f * o[i].z;
-        num[3] = num[3] * a + f * o[i].w;
+        for (int i = 0; i < N; ++i)
+          if (c0 + i * SLICES <= last) add(ml[i].x, ml[i].y, o[i]);
       }
     }
+    if constexpr (SLICES > 1) {
+      __syncthreads();  // the sums of the rows before have been read
+      part[slice][0][t] = den != den ? den : big;
+      part[slice][1][t] = den;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) part[slice][2 + i][t] = num[i];
+      __syncthreads();
+      if (slice > 0) continue;
+      for (int k = 1; k < SLICES; ++k)
+        add(part[k][0][t], part[k][1][t],
+            make_float4(part[k][2][t], part[k][3][t], part[k][4][t], part[k][5][t]));
+    }
+    if (r >= e.w) continue;
     const float inv = den > 0.f || den != den ? 1.f / den : 0.f;
     T* out = static_cast<T*>(p.out) +
              (static_cast<size_t>(e.x + (r >> p.group_shift)) * p.num_heads +
