@@ -179,9 +179,10 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream):
+def _stream(stream, here=None):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(
+            torch.cuda.current_device() if here is None else here)
     return stream.cuda_stream
 
 
@@ -658,17 +659,19 @@ def paged_attn_prefill_fp8(out, q, k_cache, v_cache, block_tables, context_lens,
            "paged_attn_prefill_fp8")
 
 
-def _same_device(*tensors):
+def _here():
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+
+
+def _same_device(here, *tensors):
     """All tensors (Nones left out) on the calling thread's current device."""
-    here = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != here:
             raise ValueError("all tensors must be on the current CUDA device (%d)" % here)
 
 
-def _devs(names, tensors, dtype=None):
+def _devs(here, names, tensors, dtype=None):
     """Every tensor contiguous, of the dtype if given, and on the current device."""
-    here = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
     for t in tensors:
         if (t.get_device() != here or not t.is_contiguous()
                 or (dtype is not None and t.dtype != dtype)):
@@ -677,120 +680,21 @@ def _devs(names, tensors, dtype=None):
         return
     for n, t in zip(names, tensors):
         _dev(t, n, dtype)
-    _same_device(*tensors)
+    _same_device(here, *tensors)
 
 
-def _tree_args(out, q, k_cache, v_cache, block_tables, context_lens, query_start, parents,
+def _tree_args(here, out, q, k_cache, v_cache, block_tables, context_lens, query_start, parents,
                num_kv_heads, block_size, dev_err):
-    _devs(("out", "q", "k_cache", "v_cache"), (out, q, k_cache, v_cache))
-    _devs(("block_tables", "context_lens", "query_start", "parents"),
+    _devs(here, ("out", "q", "k_cache", "v_cache"), (out, q, k_cache, v_cache))
+    _devs(here, ("block_tables", "context_lens", "query_start", "parents"),
           (block_tables, context_lens, query_start, parents), torch.int32)
-    _same_device(dev_err)
-    t, h, d = q.shape
-    num_blocks, hkv, bs, dk = k_cache.shape
-    s = context_lens.shape[0]
-    if (hkv, bs, dk) != (num_kv_heads, block_size, d) or out.shape != q.shape:
-        raise ValueError("shape mismatch")
-    if query_start.shape != (s + 1,) or block_tables.shape[0] != s:
-        raise ValueError("query_start must be [S+1], block_tables [S, max_blocks]")
-    if q.dtype != k_cache.dtype or out.dtype != q.dtype:
-        raise TypeError("q, out and caches must share a dtype")
-    if plan is not None:
-        pa, (ws_ptr, ws_bytes, _ws) = _plan_args(plan, workspace, q.device, stream)
-        _check(_paged_attn_prefill_planned(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                           _ptr(block_tables), _ptr(context_lens),
-                                           _ptr(query_start), *pa, float(scale), s, t, h, hkv, d,
-                                           bs, block_tables.shape[1], max_context_len,
-                                           max_query_len, num_blocks, _dtype_code(q), ws_ptr,
-                                           ws_bytes, _ptr(dev_err), _stream(stream)),
-               "paged_attn_prefill_planned")
-        return
-    _check(_paged_attn_prefill(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                               _ptr(block_tables), _ptr(context_lens), _ptr(query_start),
-                               float(scale), s, t, h, hkv, d, bs, block_tables.shape[1],
-                               max_context_len, max_query_len, num_blocks, _dtype_code(q),
-                               _ptr(dev_err), _stream(stream)),
-           "paged_attn_prefill")
-
-
-def paged_attn_prefill_fp8(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
-                           scale, k_scales, v_scales, num_kv_heads, block_size, max_context_len,
-                           max_query_len, dev_err=None, stream=None, plan=None, workspace=None):
-    """Chunked-prefill attention over E4M3 caches (values = code * scale of the
-    kv head); q and out are 16-bit.  ``plan`` and ``workspace`` as for
-    paged_attn_prefill.  See include/pagedkv.h."""
-    for n, t in (("out", out), ("q", q), ("k_cache", k_cache), ("v_cache", v_cache)):
-        _dev(t, n)
-    _dev(block_tables, "block_tables", torch.int32)
-    _dev(context_lens, "context_lens", torch.int32)
-    _dev(query_start, "query_start", torch.int32)
-    t, h, d = q.shape
-    num_blocks, hkv, bs, dk = k_cache.shape
-    s = context_lens.shape[0]
-    if (hkv, bs, dk) != (num_kv_heads, block_size, d) or out.shape != q.shape:
-        raise ValueError("shape mismatch")
-    if query_start.shape != (s + 1,) or block_tables.shape[0] != s:
-        raise ValueError("query_start must be [S+1], block_tables [S, max_blocks]")
-    if _cache_dtype_code(k_cache) != FP8_E4M3 or v_cache.dtype != k_cache.dtype:
-        raise TypeError("E4M3 caches must be uint8 (or float8_e4m3fn)")
-    if out.dtype != q.dtype:
-        raise TypeError("q and out must share a dtype")
-    ks, vs = _scales_for(k_scales, v_scales, hkv, q.device, stream)
-    if plan is not None:
-        pa, (ws_ptr, ws_bytes, _ws) = _plan_args(plan, workspace, q.device, stream)
-        _check(_paged_attn_prefill_fp8_planned(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                               _ptr(block_tables), _ptr(context_lens),
-                                               _ptr(query_start), *pa, float(scale), _ptr(ks),
-                                               _ptr(vs), s, t, h, hkv, d, bs,
-                                               block_tables.shape[1], max_context_len,
-                                               max_query_len, num_blocks, _dtype_code(q), ws_ptr,
-                                               ws_bytes, _ptr(dev_err), _stream(stream)),
-               "paged_attn_prefill_fp8_planned")
-        return
-    _check(_paged_attn_prefill_fp8(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                   _ptr(block_tables), _ptr(context_lens), _ptr(query_start),
-                                   float(scale), _ptr(ks), _ptr(vs), s, t, h, hkv, d, bs,
-                                   block_tables.shape[1], max_context_len, max_query_len,
-                                   num_blocks, _dtype_code(q), _ptr(dev_err), _stream(stream)),
-           "paged_attn_prefill_fp8")
-
-
-def _same_device(*tensors):
-    """All tensors (Nones left out) on the calling thread's current device."""
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != here:
-            raise ValueError("all tensors must be on the current CUDA device (%d)" % here)
-
-
-def _devs(names, tensors, dtype=None):
-    """Every tensor contiguous, of the dtype if given, and on the current device."""
-    here = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
-    for t in tensors:
-        if (t.get_device() != here or not t.is_contiguous()
-                or (dtype is not None and t.dtype != dtype)):
-            break
-    else:
-        return
-    for n, t in zip(names, tensors):
-        _dev(t, n, dtype)
-    _same_device(*tensors)
-
-
-def _tree_args(out, q, k_cache, v_cache, block_tables, context_lens, query_start, parents,
-               num_kv_heads, block_size, dev_err):
-    for n, t in (("out", out), ("q", q), ("k_cache", k_cache), ("v_cache", v_cache)):
-        _dev(t, n)
-    for n, t in (("block_tables", block_tables), ("context_lens", context_lens),
-                 ("query_start", query_start), ("parents", parents)):
-        _dev(t, n, torch.int32)
-    _same_device(out, q, k_cache, v_cache, block_tables, context_lens, query_start, parents,
-                 dev_err)
-    t, h, d = q.shape
-    num_blocks, hkv, bs, dk = k_cache.shape
-    s = context_lens.shape[0]
-    if ((hkv, bs, dk) != (num_kv_heads, block_size, d) or out.shape != q.shape
-            or v_cache.shape != k_cache.shape):
+    _same_device(here, dev_err)
+    shape, cache = q.shape, k_cache.shape
+    t, h, d = shape
+    num_blocks, hkv, bs, dk = cache
+    s, = context_lens.shape
+    if ((hkv, bs, dk) != (num_kv_heads, block_size, d) or out.shape != shape
+            or v_cache.shape != cache):
         raise ValueError("shape mismatch")
     if (query_start.shape != (s + 1,) or block_tables.dim() != 2 or block_tables.shape[0] != s
             or parents.shape != (t,)):
@@ -819,7 +723,7 @@ def _tree_workspace(workspace, s, h, hkv, d, max_context_len, max_query_len, dev
         with torch.cuda.stream(stream):   # memory of the stream that writes it
             return torch.empty(need, dtype=torch.uint8, device=device), need
     _dev(workspace, "workspace")
-    _same_device(workspace)
+    _same_device(torch.cuda.current_device(), workspace)
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -831,8 +735,10 @@ def paged_attn_tree(out, q, k_cache, v_cache, block_tables, context_lens, query_
     sequence), query_start [S+1], parents int32 [T] (index within the tree, -1
     for a child of the history); ``workspace`` is allocated if None.  See
     include/pagedkv.h."""
-    s, t, h, d, num_blocks = _tree_args(out, q, k_cache, v_cache, block_tables, context_lens,
-                                        query_start, parents, num_kv_heads, block_size, dev_err)
+    here = _here()
+    s, t, h, d, num_blocks = _tree_args(here, out, q, k_cache, v_cache, block_tables,
+                                        context_lens, query_start, parents, num_kv_heads,
+                                        block_size, dev_err)
     if q.dtype != k_cache.dtype:
         raise TypeError("q, out and caches must share a dtype")
     ws, ws_bytes = _tree_workspace(workspace, s, h, num_kv_heads, d, max_context_len,
@@ -841,7 +747,7 @@ def paged_attn_tree(out, q, k_cache, v_cache, block_tables, context_lens, query_
                             _ptr(context_lens), _ptr(query_start), _ptr(parents), float(scale), s,
                             t, h, num_kv_heads, d, block_size, block_tables.shape[1],
                             max_context_len, max_query_len, num_blocks, _dtype_code(q),
-                            _ptr(ws), ws_bytes, _ptr(dev_err), _stream(stream)),
+                            _ptr(ws), ws_bytes, _ptr(dev_err), _stream(stream, here)),
            "paged_attn_tree")
 
 
@@ -851,12 +757,14 @@ def paged_attn_tree_fp8(out, q, k_cache, v_cache, block_tables, context_lens, qu
                         workspace=None):
     """paged_attn_tree over E4M3 caches (values = code * scale of the kv head);
     q and out are 16-bit.  See include/pagedkv.h."""
-    s, t, h, d, num_blocks = _tree_args(out, q, k_cache, v_cache, block_tables, context_lens,
-                                        query_start, parents, num_kv_heads, block_size, dev_err)
+    here = _here()
+    s, t, h, d, num_blocks = _tree_args(here, out, q, k_cache, v_cache, block_tables,
+                                        context_lens, query_start, parents, num_kv_heads,
+                                        block_size, dev_err)
     if _cache_dtype_code(k_cache) != FP8_E4M3:
         raise TypeError("E4M3 caches must be uint8 (or float8_e4m3fn)")
     ks, vs = _scales_for(k_scales, v_scales, num_kv_heads, q.device, stream)
-    _same_device(ks, vs)
+    _same_device(here, ks, vs)
     ws, ws_bytes = _tree_workspace(workspace, s, h, num_kv_heads, d, max_context_len,
                                    max_query_len, q.device, stream)
     _check(_paged_attn_tree_fp8(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
@@ -864,7 +772,7 @@ def paged_attn_tree_fp8(out, q, k_cache, v_cache, block_tables, context_lens, qu
                                 _ptr(parents), float(scale), _ptr(ks), _ptr(vs), s, t, h,
                                 num_kv_heads, d, block_size, block_tables.shape[1],
                                 max_context_len, max_query_len, num_blocks, _dtype_code(q),
-                                _ptr(ws), ws_bytes, _ptr(dev_err), _stream(stream)),
+                                _ptr(ws), ws_bytes, _ptr(dev_err), _stream(stream, here)),
            "paged_attn_tree_fp8")
 
 
@@ -894,11 +802,13 @@ def verify_draft(accepted, num_accepted, next_token, target_probs, draft_tokens,
     the token that follows into next_token [S].  draft_probs [T, V] are the
     distributions the children were drawn from; None takes the draft as
     certain of its tokens.  See include/pagedkv.h."""
-    _devs(("accepted", "num_accepted", "next_token", "draft_tokens", "parents", "query_start"),
+    here = _here()
+    _devs(here, ("accepted", "num_accepted", "next_token", "draft_tokens", "parents",
+                 "query_start"),
           (accepted, num_accepted, next_token, draft_tokens, parents, query_start), torch.int32)
-    _devs(("accept_uniforms", "sample_uniforms"), (accept_uniforms, sample_uniforms),
+    _devs(here, ("accept_uniforms", "sample_uniforms"), (accept_uniforms, sample_uniforms),
           torch.float32)
-    _same_device(target_probs, draft_probs, dev_err)
+    _same_device(here, target_probs, draft_probs, dev_err)
     if target_probs.dim() != 2:
         raise ValueError("target_probs must be [T, vocab]")
     t, v = target_probs.shape
@@ -916,7 +826,7 @@ def verify_draft(accepted, num_accepted, next_token, target_probs, draft_tokens,
     _check(_verify_draft(_ptr(accepted), _ptr(num_accepted), _ptr(next_token), _ptr(target_probs),
                          stride, _ptr(draft_probs), dstride, _ptr(draft_tokens), _ptr(parents),
                          _ptr(query_start), _ptr(accept_uniforms), _ptr(sample_uniforms), s, t,
-                         max_query_len, v, code, _ptr(dev_err), _stream(stream)),
+                         max_query_len, v, code, _ptr(dev_err), _stream(stream, here)),
            "verify_draft")
 
 
@@ -925,10 +835,11 @@ def compact_accepted(k_cache, v_cache, block_tables, context_lens, query_start, 
     """Move the K/V of each tree's kept nodes (accepted [S, max_query_len] and
     num_accepted [S], as verify_draft writes them) to the front of the tree's
     cache positions, in place.  16-bit or E4M3 caches.  See include/pagedkv.h."""
-    _devs(("k_cache", "v_cache"), (k_cache, v_cache))
-    _devs(("block_tables", "context_lens", "query_start", "accepted", "num_accepted"),
+    here = _here()
+    _devs(here, ("k_cache", "v_cache"), (k_cache, v_cache))
+    _devs(here, ("block_tables", "context_lens", "query_start", "accepted", "num_accepted"),
           (block_tables, context_lens, query_start, accepted, num_accepted), torch.int32)
-    _same_device(dev_err)
+    _same_device(here, dev_err)
     if v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape:
         raise ValueError("k_cache and v_cache must match")
     num_blocks, hkv, bs, d = k_cache.shape
@@ -940,7 +851,7 @@ def compact_accepted(k_cache, v_cache, block_tables, context_lens, query_start, 
     _check(_compact_accepted(_ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
                              _ptr(query_start), _ptr(accepted), _ptr(num_accepted), s,
                              accepted.shape[1], hkv, d, bs, block_tables.shape[1], num_blocks,
-                             _cache_dtype_code(k_cache), _ptr(dev_err), _stream(stream)),
+                             _cache_dtype_code(k_cache), _ptr(dev_err), _stream(stream, here)),
            "compact_accepted")
 
 
