@@ -38,25 +38,32 @@ TreeEntry tree_entry(bool fp8, int qt) {
   return qt == 1 ? tree_entry<D, DT, false, 1>() : tree_entry<D, DT, false, 2>();
 }
 
-// Two query tiles a CTA once a unit can have more than 128 rows, as they share
-// each K/V tile; and over E4M3, whose tiles, held twice, leave room for one CTA an
-// SM, with two groups of softmax warps that take a smaller unit's tiles in turn.
-TreeEntry tree_entry(int head_dim, pkv_dtype dt, bool fp8, int max_rows) {
-  const int qt = max_rows > 128 ? 2 : 1;
-  if (head_dim == 128)
-    return dt == PKV_FP16 ? tree_entry<128, Fp16>(fp8, qt) : tree_entry<128, Bf16>(fp8, qt);
-  return dt == PKV_FP16 ? tree_entry<64, Fp16>(fp8, qt) : tree_entry<64, Bf16>(fp8, qt);
-}
-
 // Whether units are left whole, which spares the merge kernel and, with no more
 // units than CTAs, the scan of the lengths: where a unit has few tiles, and more
 // of them the better the units fill the GPU.  Measured on B200 (us, cut / whole;
-// GQA of 8 kv heads): 1 sequence of 512 tokens 12.4 / 13.9, of 768 13.5 / 17.2;
-// 8 of 700 17.9 / 16.9, of 1200 19.8 / 24.1; 32 of 700 26.9 / 21.9, of 1200
-// 40.5 / 34.9.
+// GQA of 8 kv heads): 1 sequence of 512 tokens 12.0 / 10.8, of 768 12.6 / 13.5; 4 of
+// 768 17.3 / 13.6; 8 of 900 18.8 / 16.3; 32 of 700 26.9 / 21.9, of 1200 40.5 / 34.9.
 bool tree_whole(long long units, int max_context_len) {
   const int tiles = (max_context_len + kTreeKeys - 1) / kTreeKeys;
-  return tiles <= 6 + std::min(units / 12, 14LL);
+  return tiles <= std::min(11 + units / 12, 20LL);
+}
+
+// Two query tiles and two groups of softmax warps a CTA, one CTA an SM: once a unit
+// can have more than 128 rows, as its query tiles share each K/V tile; over E4M3,
+// whose tiles, held twice, leave room for one CTA an SM; for whole units that are no
+// more than the SMs, as the groups take a unit's tiles in turn (1 sequence of 300
+// tokens 10.1 -> 8.9 us, 16 of 700 16.8 -> 15.0); and from 64 rows a unit, where the
+// deeper ring of tiles outlasts a unit's change (GQA chat batch 69 -> 66).  Else one
+// query tile and two CTAs an SM (LLaMA-7B batch, 16 rows a unit: 163 -> 105 us; 64
+// sequences of 700 tokens, 32 rows: 59 -> 43).
+TreeEntry tree_entry(int head_dim, pkv_dtype dt, bool fp8, int num_seqs, int num_kv_heads,
+                     int max_rows, int max_context_len) {
+  const long long units = static_cast<long long>(num_seqs) * num_kv_heads;  // of one query tile
+  const int qt =
+      fp8 || max_rows > 64 || (units <= kSms && tree_whole(units, max_context_len)) ? 2 : 1;
+  if (head_dim == 128)
+    return dt == PKV_FP16 ? tree_entry<128, Fp16>(fp8, qt) : tree_entry<128, Bf16>(fp8, qt);
+  return dt == PKV_FP16 ? tree_entry<64, Fp16>(fp8, qt) : tree_entry<64, Bf16>(fp8, qt);
 }
 
 // CTAs of a launch: no more than are resident, nor than the longest batch
@@ -64,7 +71,7 @@ bool tree_whole(long long units, int max_context_len) {
 int tree_ctas(int resident, int rows, int num_seqs, int group, int num_kv_heads,
               int max_context_len, int max_query_len) {
   const long long tiles =
-      2LL * ((max_context_len + kTreeKeys - 1) / kTreeKeys + kTreeUnitCost);  // positions
+      2LL * ((max_context_len + kTreeKeys - 1) / kTreeKeys + tree_unit_cost(rows));  // positions
   const long long units =
       static_cast<long long>(num_seqs) * ((max_query_len * group + rows - 1) / rows);
   // units * kv heads * tiles, without its overflow
@@ -113,7 +120,8 @@ pkv_status tree_launch(void* out, const void* q, const void* k_cache, const void
       !aligned4(block_tables, context_lens, query_start, parents, k_scales, v_scales, dev_err))
     return PKV_ERR_INVALID_ARG;
   const int max_rows = max_query_len * group;
-  const TreeEntry e = tree_entry(head_dim, dtype, fp8, max_rows);
+  const TreeEntry e = tree_entry(head_dim, dtype, fp8, num_seqs, num_kv_heads, max_rows,
+                                 max_context_len);
   const int ctas = tree_ctas(e.ctas, e.rows, num_seqs, group, num_kv_heads, max_context_len,
                              max_query_len);
   const int max_rts = (max_rows + e.rows - 1) / e.rows;
@@ -197,7 +205,8 @@ extern "C" size_t pkv_paged_attn_tree_workspace_bytes(int num_seqs, int num_head
   if (group > 8) return 0;
   size_t most = 0;
   for (const bool fp8 : {false, true}) {
-    const TreeEntry e = tree_entry(head_dim, PKV_FP16, fp8, max_query_len * group);
+    const TreeEntry e = tree_entry(head_dim, PKV_FP16, fp8, num_seqs, num_kv_heads,
+                                   max_query_len * group, max_context_len);
     const int ctas = tree_ctas(e.ctas, e.rows, num_seqs, group, num_kv_heads, max_context_len,
                                max_query_len);
     const long long rts = (max_query_len * group + e.rows - 1) / e.rows;

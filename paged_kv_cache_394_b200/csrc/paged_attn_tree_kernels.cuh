@@ -11,18 +11,18 @@
 // What bounds it: K and V are read once per unit, 4 D bytes a key (2 D over
 // E4M3), against 4 D multiply-adds per key and row.  At 128 rows the MMAs of a
 // 64-key tile take about half the time that HBM needs to bring it to one of 148
-// SMs, so up to 128 rows a unit is bound by memory and QT = 1 (one 128-row query
-// tile) runs two CTAs an SM, one's softmax under the other's loads.  More rows
-// take QT = 2: two query tiles share each K/V tile, one CTA an SM, bound by
-// softmax and MMA.  E4M3 caches take QT = 2 always: their tiles lie in shared
-// memory twice, as codes and as fp16, so one CTA fits, and its two groups of
-// softmax warps take the tiles of a unit of up to 128 rows in turn.  What bounds
-// them is shared memory: codes in, out and back as fp16, and the MMAs' reads are
-// about 130 KB a tile, 1024 cycles at 128 bytes each, where HBM needs 705.
+// SMs, so up to 128 rows a unit is bound by memory, and softmax runs under the
+// loads: QT = 1 (one 128-row query tile) has two CTAs an SM; QT = 2 one with two
+// groups of softmax warps, which take the tiles of such a unit in turn.  More rows
+// take QT = 2 with a query tile a group, sharing each K/V tile, bound by softmax and
+// MMA.  (paged_attn_tree.cu chooses.)  E4M3 caches take QT = 2 always: their tiles
+// lie in shared memory twice, as codes and as fp16, so one CTA fits an SM.  Codes in,
+// out and back as fp16, and the MMAs' reads are about 130 KB a tile there, 1024
+// cycles at 128 bytes each, where HBM needs 705.
 //
 // Split: the tiles of all units lie on one line, every sequence's units one
 // after the other, and CTA c takes the c-th of gridDim.x equal stretches of it,
-// whatever the lengths.  (A unit counts kTreeUnitCost tiles more than it has,
+// whatever the lengths.  (A unit counts tree_unit_cost() tiles more than it has,
 // for its query tile, pipeline fill and output.)  A unit that lies in one
 // stretch is written out directly; pieces of a cut unit go to the workspace as
 // (max, sum, unnormalised o) and paged_attn_tree_merge_kernel joins them.  Units of
@@ -86,10 +86,11 @@ struct TreeParams {
   float* ws_o;    // [pieces][D / 4][ROWS][4]
 };
 
-// What a unit costs beside its tiles, in tiles.  Measured on B200 (us; 4 / 5 / 6):
-// GQA chat batch 74.1 / 73.4 / 72.2, the LLaMA-7B batch 104.4 / 104.6 / 105.7, the
-// E4M3 batch 77.7 / 75.8 / 75.4.
-constexpr int kTreeUnitCost = 6;
+// What a unit costs beside its tiles, in tiles, of which a CTA of two query tiles,
+// alone on its SM, does nearly twice as many in the time.  Measured on B200 (us):
+// LLaMA-7B batch, one query tile, 104.7 / 104.1 / 105.4 at 4 / 5 / 6; two query
+// tiles at 5 / 7 / 10: GQA chat 71.7 / 64.5 / 65.8, E4M3 68.3 / 67.2 / 68.9.
+__host__ __device__ constexpr int tree_unit_cost(int rows) { return rows > 128 ? 7 : 5; }
 // The shortest stretch worth a CTA (2 / 6: one sequence of 1200 tokens 15.3 / 15.9
 // us, batches alike).
 constexpr int kTreeMinTiles = 2;
@@ -124,17 +125,6 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
-// The larger of two 16-bit pairs, a NaN losing to a number.
-__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, Fp16) {
-  const __half2 m = __hmax2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&m);
-}
-__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, Bf16) {
-  const __nv_bfloat162 m =
-      __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&m);
-}
-
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -155,9 +145,10 @@ struct TreeLens {
 // Positions on the line: a unit's cost beside its tiles, then its tiles, each
 // of them for every query tile of the unit.  `rows` of a unit, of 128 each.
 __device__ __forceinline__ int tree_per(int rows) { return rows > 128 ? 2 : 1; }
+template <int ROWS>
 __device__ __forceinline__ int tree_span(const TreeParams& p, int ctx, int rows) {
   return p.whole_units ? 1
-                       : ((ctx + kTreeKeys - 1) / kTreeKeys + kTreeUnitCost) * tree_per(rows);
+                       : ((ctx + kTreeKeys - 1) / kTreeKeys + tree_unit_cost(ROWS)) * tree_per(rows);
 }
 __device__ __forceinline__ TreeLens tree_lens(const TreeParams& p, int seq) {
   return {p.context_lens[seq], p.query_start[seq], p.query_start[seq + 1]};
@@ -188,7 +179,7 @@ template <int ROWS>
 __device__ __forceinline__ int tree_head_span(const TreeParams& p, const TreeSeq& s) {
   const int rows = s.q_len << p.group_shift;
   const int full = rows / ROWS, rest = rows % ROWS;
-  return full * tree_span(p, s.ctx, ROWS) + (rest > 0 ? tree_span(p, s.ctx, rest) : 0);
+  return full * tree_span<ROWS>(p, s.ctx, ROWS) + (rest > 0 ? tree_span<ROWS>(p, s.ctx, rest) : 0);
 }
 
 // Walks a CTA's stretch.  Every role walks on its own.  The lengths of the
@@ -215,7 +206,7 @@ struct TreeWalk {
       const int nt = (s.ctx + kTreeKeys - 1) / kTreeKeys;
       const int rows = (s.q_len << p.group_shift) - rt * ROWS;
       const int per = tree_per(min(rows, ROWS));
-      const int span = tree_span(p, s.ctx, min(rows, ROWS));
+      const int span = tree_span<ROWS>(p, s.ctx, min(rows, ROWS));
       const int take = min(left, span - at);
       it.seq = seq;
       it.ctx = s.ctx;
@@ -225,9 +216,9 @@ struct TreeWalk {
       it.rt = rt;
       it.nt = nt;
       // a tile is the CTA's whose stretch holds its first position
-      it.t0 = p.whole_units ? 0 : max(0, (at + per - 1) / per - kTreeUnitCost);
-      it.t1 = p.whole_units ? nt : max(0, (at + take + per - 1) / per - kTreeUnitCost);
-      it.lead = max(0, at - kTreeUnitCost * per);
+      it.t0 = p.whole_units ? 0 : max(0, (at + per - 1) / per - tree_unit_cost(ROWS));
+      it.t1 = p.whole_units ? nt : max(0, (at + take + per - 1) / per - tree_unit_cost(ROWS));
+      it.lead = max(0, at - tree_unit_cost(ROWS) * per);
       left -= take;
       at += take;
       if (at == span) {
@@ -291,10 +282,6 @@ struct TreeTraits {
   static constexpr int QCOLS = 256;
   static constexpr uint32_t TMEM_COLS = QT * QCOLS;
   static constexpr float kRescaleThreshold = 8.f;
-  // P before its maximum is looked at (see the softmax).  Measured on B200 (us):
-  // GQA chat batch 76 -> 71, its E4M3 form 73 -> 70; but two query tiles of bf16
-  // (long contexts) 264 -> 281.
-  static constexpr bool kAhead = QT == 1 || kFp8;
   static_assert(MIN_BLOCKS * (1024 + 1024 + SMEM) <= 228 * 1024, "shared memory per SM");
   static size_t smem_bytes() { return 1024 + static_cast<size_t>(SMEM); }
 };
@@ -428,7 +415,7 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
           TreeSeq seq;
           tree_seq(p, x, seq, false);
           const int head = tree_head_span<ROWS>(p, seq);
-          const int full = tree_span(p, seq.ctx, ROWS);  // every row tile but the last
+          const int full = tree_span<ROWS>(p, seq.ctx, ROWS);  // every row tile but the last
           const int kvh = small ? static_cast<int>(at) / head : static_cast<int>(at / head);
           const int in_head = static_cast<int>(at - static_cast<long long>(kvh) * head);
           const int rt = min(in_head / full, ((seq.q_len << p.group_shift) - 1) / ROWS);
@@ -860,62 +847,40 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
             tc::f2_unpack(sum2[1], a[2], a[3]);
             return (a[0] + a[1]) + (a[2] + a[3]);
           };
-          // Most tiles move no maximum: P is made with the one at hand, and only
-          // where a value passes 2^8 (kRescaleThreshold), or a row has none yet,
-          // is the tile read again and its maximum taken.
-          float alpha = 1.f, sum;
-          bool take_max =
-              !Tr::kAhead || __any_sync(kFullMask, cut || !(mult0 > 0.f) || m == -INFINITY);
-          for (;;) {
-            float s[2][32];
-            tmem_ld32(sbuf, s[0]);
-            tmem_ld32(sbuf + 32, s[1]);
-            tc::tmem_wait_ld();
-            if (take_max) {
-              if (cut || !(mult0 > 0.f)) {
-                const unsigned long long bits = window(t);
-                const uint32_t b0 = static_cast<uint32_t>(bits);
-                const uint32_t b1 = static_cast<uint32_t>(bits >> 32);
-                const float f = mult0 > 0.f ? 1.f : mult0;
+          float s[2][32];
+          tmem_ld32(sbuf, s[0]);
+          tmem_ld32(sbuf + 32, s[1]);
+          tc::tmem_wait_ld();
+          if (cut || !(mult0 > 0.f)) {
+            const unsigned long long bits = window(t);
+            const uint32_t b0 = static_cast<uint32_t>(bits);
+            const uint32_t b1 = static_cast<uint32_t>(bits >> 32);
+            const float f = mult0 > 0.f ? 1.f : mult0;
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                  s[0][c] = b0 & (1u << c) ? s[0][c] * f : -INFINITY;
-                  s[1][c] = b1 & (1u << c) ? s[1][c] * f : -INFINITY;
-                }
-              }
-              float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-              for (int c = 0; c < 32; c += 4) {
-                mx4[0] = tc::max3(mx4[0], s[0][c], s[0][c + 1]);
-                mx4[1] = tc::max3(mx4[1], s[0][c + 2], s[0][c + 3]);
-                mx4[2] = tc::max3(mx4[2], s[1][c], s[1][c + 1]);
-                mx4[3] = tc::max3(mx4[3], s[1][c + 2], s[1][c + 3]);
-              }
-              const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * mult;
-              if (mx > m + Tr::kRescaleThreshold) {
-                alpha = exp2_approx(m - mx);  // 0 on the first tile (m = -inf)
-                m = mx;
-              }
+            for (int c = 0; c < 32; ++c) {
+              s[0][c] = b0 & (1u << c) ? s[0][c] * f : -INFINITY;
+              s[1][c] = b1 & (1u << c) ? s[1][c] * f : -INFINITY;
             }
-            const float neg_m = m == -INFINITY ? 0.f : -m;
-            uint64_t sum2[2] = {0, 0};
-            weigh(s[0], 0, neg_m, sum2);
-            weigh(s[1], 1, neg_m, sum2);
-            sum = total(sum2);
-            if (take_max) break;
-            uint32_t top[4] = {w[0], w[1], w[2], w[3]};
-#pragma unroll
-            for (int c = 4; c < 32; c += 4)
-#pragma unroll
-              for (int u = 0; u < 4; ++u) top[u] = max2(top[u], w[c + u], MT());
-            const uint32_t most = max2(max2(top[0], top[1], MT()), max2(top[2], top[3], MT()), MT());
-            constexpr uint32_t kMost = Tr::kBf16 ? 0x4380u : 0x5C00u;  // 2^8, as a bit pattern
-            if (!__any_sync(kFullMask,
-                            active && ((most & 0xffffu) > kMost || (most >> 16) > kMost)))
-              break;
-            take_max = true;
           }
-          l = l * alpha + sum;
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            mx4[0] = tc::max3(mx4[0], s[0][c], s[0][c + 1]);
+            mx4[1] = tc::max3(mx4[1], s[0][c + 2], s[0][c + 3]);
+            mx4[2] = tc::max3(mx4[2], s[1][c], s[1][c + 1]);
+            mx4[3] = tc::max3(mx4[3], s[1][c + 2], s[1][c + 3]);
+          }
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * mult;
+          float alpha = 1.f;
+          if (mx > m + Tr::kRescaleThreshold) {
+            alpha = exp2_approx(m - mx);  // 0 on the first tile (m = -inf)
+            m = mx;
+          }
+          const float neg_m = m == -INFINITY ? 0.f : -m;
+          uint64_t sum2[2] = {0, 0};
+          weigh(s[0], 0, neg_m, sum2);
+          weigh(s[1], 1, neg_m, sum2);
+          l = l * alpha + total(sum2);
           // P over S: 32 columns, and 32 of what bf16 rounded off
 #pragma unroll
           for (int h = 0; h < 2; ++h) {

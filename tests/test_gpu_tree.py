@@ -63,6 +63,23 @@ def test_every_shape_in_pieces(pk, d, bs, g, dtype, fp8):
     t.check(some_rows(w, 20))
 
 
+# up to 64 rows a unit, cut; and more of them, whole, than there are SMs
+@pytest.mark.parametrize("d,bs,g,dtype", SHAPES)
+def test_every_shape_of_few_rows(pk, d, bs, g, dtype):
+    most = 64 // g
+    w = tree_workload([1700, 33, 64, 900, 0], [most // 2, 0, most, 3, most], 2 * g, 2, d, bs,
+                      dtype, seed=5 * d + bs + g)
+    t = TreeOnDevice(pk, w)
+    assert t.run() == 0
+    t.check(some_rows(w, 20))
+    hist = [7 * i % 150 for i in range(80)]
+    w = tree_workload(hist, [i % (most // 4 + 1) for i in range(80)], 2 * g, 2, d, bs, dtype,
+                      seed=6 * d + bs + g)
+    t = TreeOnDevice(pk, w)
+    assert t.run() == 0
+    t.check(some_rows(w, 20))
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_many_sequences(pk, fp8):
     """More sequences than a CTA has threads, most of one tile, some empty, one
@@ -134,7 +151,7 @@ def test_chain_is_prefill_and_one_node_is_decode(pk):
 
 
 @pytest.mark.parametrize("hist,heads", [([70, 20], 8), ([1130, 20], 8), ([1130, 650], 2),
-                                        ([70, 20], 2)])
+                                        ([70, 20], 2), ([2100, 950], 4)])
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("d,dtype", [(128, "bf16"), (128, "fp16"), (64, "fp16")])
 def test_what_a_row_does_not_see_does_not_enter_it(pk, d, dtype, fp8, hist, heads):
