@@ -307,12 +307,16 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
   auto bar_s = [&](int q, int b) { return bar(Tr::B_Q + 8 * q + 2 + b); };
   auto bar_p = [&](int q, int b) { return bar(Tr::B_Q + 8 * q + 4 + b); };
   auto bar_o = [&](int q, int b) { return bar(Tr::B_Q + 8 * q + 6 + b); };
-  // behind the barriers: TMEM address, where the stretch starts, the items
-  // whose V held non-finite tree elements (by parity: item + 1)
+  // behind the barriers: the TMEM address; the items whose V held non-finite tree
+  // elements (by parity); where the stretch starts
   int* words = reinterpret_cast<int*>(smem + Tr::OFF_BAR + Tr::NBAR * 8);
-  // sequence, kv head, position in the unit, length of the stretch; lengths; row tile
-  int* s_found = words + 1;
-  int* s_odd = words + 9;
+  int* s_odd = words + 2;
+  struct Found {
+    long long at;
+    int seq;
+    TreeLens lens;
+  };
+  Found* s_found = reinterpret_cast<Found*>(words + 4);
 
   const int warp = __shfl_sync(kFullMask, static_cast<int>(threadIdx.x) >> 5, 0);
   const int lane = threadIdx.x & 31;
@@ -341,7 +345,7 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
     mbar_init(bar(Tr::B_BOTH), 4);
     mbar_init(bar(Tr::B_DRAIN), 1);
     mbar_init(bar(Tr::B_DRAIN + 1), 1);
-    s_found[3] = 0;
+    s_found->seq = -1;
     s_odd[0] = s_odd[1] = 0;
     fence_mbar_init();
   }
@@ -372,77 +376,100 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
     tc::tc_fence_before();
     __syncthreads();
   } else {
-    const int per = (p.num_seqs + Tr::THREADS - 1) / Tr::THREADS;
-    const int first = min(p.num_seqs, static_cast<int>(threadIdx.x) * per);
-    const int last = min(p.num_seqs, first + per);
     auto weight = [&](const TreeLens& x, bool report) -> long long {
       TreeSeq s;
       if (!tree_seq(p, x, s, report)) return 0;
       return static_cast<long long>(tree_head_span<ROWS>(p, s)) * p.num_kv_heads;
     };
-    long long own = 0;
-    TreeLens lens = {};  // of the last of this thread's sequences
-    for (int i = first; i < last; ++i) {
-      lens = tree_lens(p, i);
-      own += weight(lens, blockIdx.x == 0);
-    }
-    long long upto = own;  // inclusive scan over the warp, then over the warps
+    auto scan = [&](long long x) {  // inclusive, over the warp
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(kFullMask, upto, o);
-      if (lane >= o) upto += x;
-    }
-    long long* sums = reinterpret_cast<long long*>(smem + Tr::OFF_SEEN);
-    if (lane == 31) sums[warp] = upto;
-    __syncthreads();
-    long long total = 0;
-    for (int w = 0; w < Tr::THREADS / 32; ++w) {
-      if (w < warp) upto += sums[w];
-      total += sums[w];
-    }
-    const bool small = total + gridDim.x < 0x7fffffff;  // 32-bit divisions, many times as fast
-    const long long even = small ? (static_cast<unsigned>(total) + gridDim.x - 1) / gridDim.x
-                                 : (total + gridDim.x - 1) / gridDim.x;
-    const long long least = p.whole_units ? 1 : kTreeMinTiles;
-    const long long each = even > least ? even : least;
-    const long long start = each * blockIdx.x;
-    if (start < upto && start >= upto - own) {
-      long long at = start - (upto - own);
-      for (int i = first; i < last; ++i) {
-        const TreeLens x = per == 1 ? lens : tree_lens(p, i);
-        const long long w = weight(x, false);
-        if (at < w) {
-          TreeSeq seq;
-          tree_seq(p, x, seq, false);
-          const int head = tree_head_span<ROWS>(p, seq);
-          const int full = tree_span<ROWS>(p, seq.ctx, ROWS);  // every row tile but the last
-          const int kvh = small ? static_cast<int>(at) / head : static_cast<int>(at / head);
-          const int in_head = static_cast<int>(at - static_cast<long long>(kvh) * head);
-          const int rt = min(in_head / full, ((seq.q_len << p.group_shift) - 1) / ROWS);
-          s_found[0] = i;
-          s_found[1] = kvh;
-          s_found[7] = rt;
-          s_found[2] = in_head - rt * full;
-          // the line's end cuts the last stretch by itself
-          s_found[3] = static_cast<int>(each < 0x7fffffff ? each : 0x7fffffff);
-          s_found[4] = x.ctx;
-          s_found[5] = x.q0;
-          s_found[6] = x.end;
-          break;
-        }
-        at -= w;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(kFullMask, x, o);
+        if (lane >= o) x += y;
       }
-    }
+      return x;
+    };
+    // the stretches' length on a line of `total`; 32-bit divisions are many times as fast
+    auto each_of = [&](long long total) {
+      const long long even = total + gridDim.x < 0x7fffffff
+                                 ? (static_cast<unsigned>(total) + gridDim.x - 1) / gridDim.x
+                                 : (total + gridDim.x - 1) / gridDim.x;
+      const long long least = p.whole_units ? 1 : kTreeMinTiles;
+      return even > least ? even : least;
+    };
     if (threadIdx.x == 0 && !p.whole_units && !p.by_unit)
       p.ws_meta[blockIdx.x] = make_int4(0, 0, 0, 0);
-    tc::tc_fence_before();
-    __syncthreads();
-    walk.seq = s_found[0];
-    walk.kvh = s_found[1];
-    walk.rt = s_found[7];
-    walk.at = s_found[2];
-    walk.ahead = {s_found[4], s_found[5], s_found[6]};
-    len = s_found[3];
+    // The sequence that the stretch starts in, and where in it.
+    long long at = 0, each = 0;
+    if (p.num_seqs <= 32) {  // every warp for itself
+      TreeLens x = {};
+      long long own = 0;
+      if (lane < p.num_seqs) {
+        x = tree_lens(p, lane);
+        own = weight(x, blockIdx.x == 0 && warp == 0);
+      }
+      const long long upto = scan(own);
+      each = each_of(__shfl_sync(kFullMask, upto, 31));
+      const long long start = each * blockIdx.x;
+      const unsigned in = __ballot_sync(kFullMask, start < upto && start >= upto - own);
+      const int from = in != 0 ? __ffs(in) - 1 : 0;
+      walk.seq = from;
+      at = start - __shfl_sync(kFullMask, upto - own, from);
+      walk.ahead = {__shfl_sync(kFullMask, x.ctx, from), __shfl_sync(kFullMask, x.q0, from),
+                    __shfl_sync(kFullMask, x.end, from)};
+      if (in == 0) each = 0;
+      tc::tc_fence_before();
+      __syncthreads();
+    } else {
+      const int per = (p.num_seqs + Tr::THREADS - 1) / Tr::THREADS;
+      const int first = min(p.num_seqs, static_cast<int>(threadIdx.x) * per);
+      const int last = min(p.num_seqs, first + per);
+      long long own = 0;
+      for (int i = first; i < last; ++i) own += weight(tree_lens(p, i), blockIdx.x == 0);
+      long long upto = scan(own);
+      long long* sums = reinterpret_cast<long long*>(smem + Tr::OFF_SEEN);
+      if (lane == 31) sums[warp] = upto;
+      __syncthreads();
+      long long total = 0;
+      for (int w = 0; w < Tr::THREADS / 32; ++w) {
+        if (w < warp) upto += sums[w];
+        total += sums[w];
+      }
+      each = each_of(total);
+      const long long start = each * blockIdx.x;
+      if (start < upto && start >= upto - own) {
+        at = start - (upto - own);
+        for (int i = first; i < last; ++i) {
+          const TreeLens x = tree_lens(p, i);
+          const long long w = weight(x, false);
+          if (at < w) {
+            s_found->seq = i;
+            s_found->lens = x;
+            s_found->at = at;
+            break;
+          }
+          at -= w;
+        }
+      }
+      tc::tc_fence_before();
+      __syncthreads();
+      walk.seq = s_found->seq;
+      walk.ahead = s_found->lens;
+      at = s_found->at;
+      if (walk.seq < 0) each = 0;
+    }
+    // the line's end cuts the last stretch by itself
+    len = static_cast<int>(each < 0x7fffffff ? each : 0x7fffffff);
+    if (len > 0) {
+      TreeSeq seq;
+      tree_seq(p, walk.ahead, seq, false);
+      const int head = tree_head_span<ROWS>(p, seq);
+      const int full = tree_span<ROWS>(p, seq.ctx, ROWS);  // every row tile but the last
+      walk.kvh = at < 0x7fffffff ? static_cast<int>(at) / head : static_cast<int>(at / head);
+      const int in_head = static_cast<int>(at - static_cast<long long>(walk.kvh) * head);
+      walk.rt = min(in_head / full, ((seq.q_len << p.group_shift) - 1) / ROWS);
+      walk.at = in_head - walk.rt * full;
+    }
   }
   tc::tc_fence_after();
   const uint32_t tmem = __shfl_sync(kFullMask, static_cast<uint32_t>(words[0]), 0);
