@@ -84,8 +84,9 @@ int tree_ctas(int resident, int rows, int num_seqs, int group, int num_kv_heads,
 
 size_t tree_ws_bytes(int ctas, int rows, int head_dim, bool whole) {
   if (whole) return 0;
-  return static_cast<size_t>(ctas) *
-         (sizeof(int4) + 2 * static_cast<size_t>(rows) * (8 + 4 * static_cast<size_t>(head_dim)));
+  return 16 + static_cast<size_t>(ctas) *
+                  (sizeof(int4) +
+                   2 * static_cast<size_t>(rows) * (8 + 4 * static_cast<size_t>(head_dim)));
 }
 
 // Validates and launches; fp8: the caches hold E4M3 codes with per-kv-head
@@ -165,11 +166,14 @@ pkv_status tree_launch(void* out, const void* q, const void* k_cache, const void
   const bool many = units * 2 * kMergeSlices <= ctas;
   p.by_unit = many;
   p.num_ctas = ctas;
+  p.out_aligned32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   p.err = dev_err;
   if (!whole) {
-    p.ws_meta = static_cast<int4*>(workspace);
-    p.ws_o = reinterpret_cast<float*>(p.ws_meta + ctas);
+    // the pieces first, on a 32-byte boundary: at most 16 bytes in
+    p.ws_o = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(workspace) + 31) &
+                                      ~static_cast<uintptr_t>(31));
     p.ws_ml = reinterpret_cast<float2*>(p.ws_o + static_cast<size_t>(ctas) * 2 * e.rows * head_dim);
+    p.ws_meta = reinterpret_cast<int4*>(p.ws_ml + static_cast<size_t>(ctas) * 2 * e.rows);
   }
   st = cuda_status(cudaFuncSetAttribute(e.fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         static_cast<int>(e.smem)));

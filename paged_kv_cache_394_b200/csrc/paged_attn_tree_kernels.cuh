@@ -74,6 +74,7 @@ struct TreeParams {
   int whole_units;  // units are not cut
   int direct;       // ... and each has its CTA: max_rts for every (sequence, kv head)
   int max_rts, num_ctas;
+  int out_aligned32;
   unsigned* err;
   // Workspace: for each CTA one merge entry and two pieces of ROWS rows.  Entry c
   // is of the unit that ended in CTA c, {first token, kv head, first CTA, rows},
@@ -83,7 +84,7 @@ struct TreeParams {
   int by_unit;
   int4* ws_meta;
   float2* ws_ml;  // (max, sum) of each row of each piece
-  float* ws_o;    // [pieces][D / 4][ROWS][4]
+  float* ws_o;    // [pieces][D / 8][ROWS][8], on a 32-byte boundary
 };
 
 // What a unit costs beside its tiles, in tiles, of which a CTA of two query tiles,
@@ -123,6 +124,13 @@ __device__ __forceinline__ bool elect_one() {
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(one));
   return one != 0;
+}
+
+// 32 bytes to a 32-byte boundary in one store.
+__device__ __forceinline__ void store32(void* dst, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a.x),
+               "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -1055,19 +1063,29 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
           if (whole) {
             T* o = static_cast<T*>(p.out) + row * D + c;
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              float x[8];
+            for (int i = 0; i < 32; i += 16) {
+              float x[8], y[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] = v[i + e] * inv;
-              *reinterpret_cast<uint4*>(o + i) = pack8(x, typename Tr::DT());
+              for (int e = 0; e < 8; ++e) x[e] = v[i + e] * inv, y[e] = v[i + 8 + e] * inv;
+              const uint4 a = pack8(x, typename Tr::DT()), b = pack8(y, typename Tr::DT());
+              if (p.out_aligned32) {
+                store32(o + i, a, b);
+              } else {
+                *reinterpret_cast<uint4*>(o + i) = a;
+                *reinterpret_cast<uint4*>(o + i + 8) = b;
+              }
             }
           } else {
-            // [D / 4][ROWS] of 4 floats: a warp's rows side by side
-            float4* o = reinterpret_cast<float4*>(p.ws_o) + piece * (D / 4) * ROWS + qt * M + r;
+            // [D / 8][ROWS] of 8 floats: a warp's rows side by side
+            uint4* o = reinterpret_cast<uint4*>(p.ws_o) + (piece * (D / 8) * ROWS + qt * M + r) * 2;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              o[(c / 4 + i) * ROWS] = make_float4(v[4 * i] * v_scale, v[4 * i + 1] * v_scale,
-                                                  v[4 * i + 2] * v_scale, v[4 * i + 3] * v_scale);
+            for (int i = 0; i < 32; i += 8) {
+              uint32_t x[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(v[i + e] * v_scale);
+              store32(o + (c + i) / 8 * ROWS * 2, make_uint4(x[0], x[1], x[2], x[3]),
+                      make_uint4(x[4], x[5], x[6], x[7]));
+            }
           }
         }
       }
@@ -1098,7 +1116,7 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
           if (whole)
             static_cast<T*>(p.out)[row * D + c] = static_cast<T>(sum);
           else
-            p.ws_o[((piece * (D / 4) + c / 4) * ROWS + qt * M + r) * 4 + c % 4] = sum;
+            p.ws_o[((piece * (D / 8) + c / 8) * ROWS + qt * M + r) * 8 + c % 8] = sum;
         }
       }
       tc::tc_fence_before();
@@ -1205,9 +1223,10 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
 // Joins the pieces of the units that lie across CTAs' stretches: with M = max m,
 //   out = sum 2^(m - M) o / sum 2^(m - M) l.
 // The piece of a unit's first CTA is that CTA's second, of every later one its
-// first.  A thread has 4 dims of a row, a warp 2 rows x 64 dims (whole sectors of
-// the pieces), and SLICES sets of threads take every SLICES-th piece and meet in
-// shared memory.  Block (i, j) takes entry i, of its groups of rows the j-th and
+// first.  A thread has 4 dims of a row, two threads a sector of the pieces, which
+// were stored 32 bytes a thread (16 at a time: LLaMA-7B batch 105.0 us instead of
+// 103.1, E4M3 66.9 instead of 65.3).  SLICES sets of threads take every SLICES-th
+// piece and meet in shared memory.  Block (i, j) takes entry i, of its groups of rows the j-th and
 // every gridDim.y-th after.  It is bound by the latency of its loads: N of them
 // are under way at once, 8 for units in many pieces, 3 where a unit has two or
 // three, which leaves 8 blocks an SM (GQA chat batch 72.9 us with 8, 68.4 with 3).
@@ -1219,14 +1238,12 @@ __global__ void __launch_bounds__(kTreeMergeThreads, SLICES > 1 ? 1 : 8)
   constexpr int PER = kTreeMergeThreads / SLICES;  // threads of a slice
   constexpr int RB = PER / (D / 4);                // rows of a block
   constexpr int N = SLICES > 1 ? 8 : 3;
-  static_assert(RB % 2 == 0, "a warp takes two rows");
   __shared__ float part[SLICES > 1 ? SLICES : 1][6][SLICES > 1 ? PER : 1];
   grid_dependency_wait();
   trigger_dependents();
   int4 e = p.ws_meta[blockIdx.x];
   const int slice = threadIdx.x / PER, t = threadIdx.x % PER;
-  const int w = t >> 5, lane = t & 31;
-  const int c4 = (w % (D / 64)) * 16 + (lane >> 1);
+  const int c4 = t % (D / 4);
   int last = static_cast<int>(blockIdx.x);
   if (p.by_unit) {
     const int seq = static_cast<int>(blockIdx.x) / (p.num_kv_heads * p.max_rts);
@@ -1241,7 +1258,7 @@ __global__ void __launch_bounds__(kTreeMergeThreads, SLICES > 1 ? 1 : 8)
                   min(ROWS, (s.q_len << p.group_shift) - rt * ROWS));
   }
   for (int r0 = static_cast<int>(blockIdx.y) * RB; r0 < e.w; r0 += RB * gridDim.y) {
-    const int r = r0 + (w / (D / 64)) * 2 + (lane & 1);
+    const int r = r0 + t / (D / 4);
     float big = -INFINITY, num[4] = {}, den = 0.f;
     auto add = [&](float m1, float l1, const float4& o) {
       const float m = m1 == -INFINITY ? big : fmaxf(big, m1);
@@ -1263,7 +1280,8 @@ __global__ void __launch_bounds__(kTreeMergeThreads, SLICES > 1 ? 1 : 8)
           const int c = min(c0 + i * SLICES, last);
           const size_t piece = static_cast<size_t>(c) * 2 + (c == e.z ? 1 : 0);
           ml[i] = p.ws_ml[piece * ROWS + r];
-          o[i] = reinterpret_cast<const float4*>(p.ws_o)[(piece * (D / 4) + c4) * ROWS + r];
+          o[i] = reinterpret_cast<const float4*>(
+              p.ws_o)[((piece * (D / 8) + c4 / 2) * ROWS + r) * 2 + c4 % 2];
         }
 #pragma unroll
         for (int i = 0; i < N; ++i)

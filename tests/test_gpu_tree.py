@@ -359,3 +359,29 @@ def test_two_runs_agree_bit_for_bit(pk):
         t.run()
         assert torch.equal(first, t.out)
 
+
+
+# rows and pieces are stored 32 bytes at a time where the addresses allow it
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("hist", [[3000, 17], [40, 9]])   # cut; whole
+def test_places_of_output_and_workspace(pk, hist, fp8):
+    w = tree_workload(hist, [20, 9], 16, 2, 128, 16, "fp16", seed=29)
+    t = TreeOnDevice(pk, w, scales=([0.0125, 0.02], [0.01, 0.03]) if fp8 else None)
+    assert t.run() == 0
+    first, n = t.out.clone(), t.out.numel()
+    need = pk.tree_workspace_bytes(w.num_seqs, w.num_heads, w.num_kv_heads, w.head_dim,
+                                   w.max_context_len, t.max_nodes)
+    assert (need > 0) == (hist[0] > 64)
+    for at in (0, 16, 32, 48):
+        ws = torch.full((at + need + 64,), 0x5A, dtype=torch.uint8, device="cuda")
+        room = torch.full((n + 64,), 7.0, dtype=first.dtype, device="cuda")
+        t.out = room[at // 2:at // 2 + n].view_as(first)
+        assert t.run(workspace=ws[at:at + need] if need else None) == 0
+        assert torch.equal(first, t.out)
+        assert (room[:at // 2] == 7.0).all() and (room[at // 2 + n:] == 7.0).all()
+        assert (ws[:at] == 0x5A).all() and (ws[at + need:] == 0x5A).all()
+    if need:
+        with pytest.raises(RuntimeError):
+            t.run(workspace=ws[:need - 1])
+        with pytest.raises(RuntimeError):
+            t.run(workspace=ws[8:8 + need])
