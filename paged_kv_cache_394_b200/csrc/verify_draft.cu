@@ -16,8 +16,10 @@
 //
 // A cluster of 1 to 8 CTAs serves a sequence.  Rank 0 gathers what the walk
 // needs (each node's parent, token, uniform, and the two probabilities of its
-// token at its parent) into every CTA's shared memory, so that all of them walk
-// alike; each warp of the cluster has its own contiguous piece of the vocabulary.
+// token at its parent) into every CTA's shared memory, once all CTAs are known to
+// have started (a cluster barrier entered first thing and waited for under those
+// loads), so that all of them walk alike; each warp of the cluster has its own
+// contiguous piece of the vocabulary.
 // A pass leaves a sum per warp; the CTAs exchange theirs through distributed
 // shared memory, and only the warp whose piece holds the next token reads that
 // piece again.  All sums are 64-bit and in a fixed order.
@@ -95,6 +97,15 @@ __device__ __forceinline__ double residual(float p, float q, double taken) {
   return fmax(fma(-taken, static_cast<double>(q), static_cast<double>(p)), 0.0);
 }
 
+// The two halves of a cluster barrier that says only that every CTA runs (nothing
+// has been written yet, so the arrival orders no memory).  Whole warps call them.
+__device__ __forceinline__ void cluster_arrive_started() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_started() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 template <class T>
 __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const VerifyParams p) {
   __shared__ VerifyShared sh;
@@ -108,39 +119,50 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
   const bool certain = p.draft == nullptr;
   const T* target = static_cast<const T*>(p.target);
   const T* draft = static_cast<const T*>(p.draft);
+  // Shared memory of another CTA may be written once that CTA has started: each
+  // arrives here, and all wait before rank 0's first remote store.
+  if (ranks > 1) cluster_arrive_started();
   grid_dependency_wait();
   trigger_dependents();
   const int q0 = p.query_start[seq];  // rank 0's reading decides what is used of it
+  int nodes = 0, up = -1, token = 0;  // rank 0: of the tree; node tid's parent and token
+  float px = 0.f, qx = 0.f, u = 0.f;
+  static_assert(PKV_MAX_TREE_NODES <= kVerifyThreads, "a thread per node");
   if (rank == 0) {
     const int end = p.query_start[seq + 1];
-    int n = end < q0 ? -1 : static_cast<int>(static_cast<unsigned>(end) - static_cast<unsigned>(q0));
-    if (n < 0 || n > p.max_query_len || q0 < 0 || q0 > p.num_tokens - n) {
+    nodes = end < q0 ? -1 : static_cast<int>(static_cast<unsigned>(end) - static_cast<unsigned>(q0));
+    if (nodes < 0 || nodes > p.max_query_len || q0 < 0 || q0 > p.num_tokens - nodes) {
       if (tid == 0) set_err(p.err, PKV_DEVERR_BAD_CONTEXT);
-      n = 0;
+      nodes = 0;
     }
-    for (int j = tid; j < n; j += kVerifyThreads) {
-      int up = p.parents[q0 + j];
-      const int x = p.tokens[q0 + j];
-      if (j == 0 ? up != -1 : up < -1 || up >= j) {
+    if (tid < nodes) {
+      up = p.parents[q0 + tid];
+      token = p.tokens[q0 + tid];
+      if (tid == 0 ? up != -1 : up < -1 || up >= tid) {
         set_err(p.err, PKV_DEVERR_BAD_TREE);
         up = -1;
       }
-      float px = 0.f, qx = 0.f;
-      if (up >= 0 && static_cast<unsigned>(x) < static_cast<unsigned>(p.vocab)) {
-        px = weight_of(target[(q0 + up) * p.target_stride + x]);
-        if (!certain) qx = weight_of(draft[(q0 + up) * p.draft_stride + x]);
+      if (up >= 0 && static_cast<unsigned>(token) < static_cast<unsigned>(p.vocab)) {
+        px = weight_of(target[(q0 + up) * p.target_stride + token]);
+        if (!certain) qx = weight_of(draft[(q0 + up) * p.draft_stride + token]);
       }
-      const float u = p.accept_u[q0 + j];
-      for (int c = 0; c < ranks; ++c) {
-        VerifyShared* to = cluster.map_shared_rank(&sh, c);
-        to->parent[j] = up;
-        to->token[j] = x;
-        to->u[j] = u;
-        to->p[j] = px;
-        to->q[j] = qx;
-      }
+      u = p.accept_u[q0 + tid];
     }
-    if (tid < ranks) cluster.map_shared_rank(&sh, tid)->n = n;
+  }
+  if (ranks > 1) {
+    __syncwarp();
+    cluster_wait_started();
+  }
+  if (rank == 0) {
+    for (int c = 0; c < ranks && tid < nodes; ++c) {
+      VerifyShared* to = cluster.map_shared_rank(&sh, c);
+      to->parent[tid] = up;
+      to->token[tid] = token;
+      to->u[tid] = u;
+      to->p[tid] = px;
+      to->q[tid] = qx;
+    }
+    if (tid < ranks) cluster.map_shared_rank(&sh, tid)->n = nodes;
   }
   cluster.sync();
   const int n = sh.n;
