@@ -32,10 +32,18 @@
 // ring of NS stages; warp 1 issues S = Q K^T into one of two TMEM buffers; warp
 // 3 issues O += P V with P read from TMEM; 4 softmax warps per query tile, a
 // thread per row (online softmax in base 2 in fp32; the reference maximum moves
-// only when a logit passes it by 2^8, so O is rarely rescaled).  P is rounded to
-// fp16, or split into two bf16 halves for bf16 caches (2^-17 of p), so that it
-// costs no accuracy next to the output's rounding.  E4M3 caches: further warps
-// widen each tile's codes to fp16 (exact) into the stage that the MMAs read.
+// only when a logit passes it by 2^8, so O is rarely rescaled).  E4M3 caches:
+// further warps widen each tile's codes to fp16 (exact) into the stage that the
+// MMAs read.
+//
+// P in 16 bits, as the MMAs take it.  bf16 caches: two bf16 halves, 2^-17 of p, which
+// the output's rounding hides.  fp16 and E4M3 caches: fp16, 2^-12 of p in earnest and
+// 2^-11 at most, as much as the output's own rounding where one key dominates and
+// less where many errors meet (two halves would double the P V MMAs).  fp16 is
+// subnormal below 2^-14, so P = 2^(x - m) with m 7 below the row's reference
+// maximum: P is normal down to 2^-21 of that maximum and off by at most 2^-32 of it
+// below, that is at most 2^-32 sum |v_k| in the output (without the 7, keys of 2^-25
+// and less vanished, however many).  The sum l takes p in fp32 before it is rounded.
 //
 // The tree's part of the keys: each row's visible nodes are a bit set, made once
 // per unit by following the parents.  What a row does not see must not enter
@@ -290,6 +298,9 @@ struct TreeTraits {
   static constexpr int QCOLS = 256;
   static constexpr uint32_t TMEM_COLS = QT * QCOLS;
   static constexpr float kRescaleThreshold = 8.f;
+  // log2 of P at the row's reference maximum: P reaches 2^15 in fp16 before a
+  // rescale, and is normal down to 2^-21 of that maximum
+  static constexpr float kBias = kBf16 ? 0.f : 7.f;
   static_assert(MIN_BLOCKS * (1024 + 1024 + SMEM) <= 228 * 1024, "shared memory per SM");
   static size_t smem_bytes() { return 1024 + static_cast<size_t>(SMEM); }
 };
@@ -907,9 +918,10 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
           }
           const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * mult;
           float alpha = 1.f;
-          if (mx > m + Tr::kRescaleThreshold) {
-            alpha = exp2_approx(m - mx);  // 0 on the first tile (m = -inf)
-            m = mx;
+          if (mx > m + (Tr::kRescaleThreshold + Tr::kBias)) {
+            const float top = mx - Tr::kBias;
+            alpha = exp2_approx(m - top);  // 0 on the first tile (m = -inf)
+            m = top;
           }
           const float neg_m = m == -INFINITY ? 0.f : -m;
           uint64_t sum2[2] = {0, 0};
