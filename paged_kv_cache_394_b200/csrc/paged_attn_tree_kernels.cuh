@@ -1269,6 +1269,11 @@ __global__ void __launch_bounds__(kTreeMergeThreads, SLICES > 1 ? 1 : 8)
                   static_cast<int>(blockIdx.x) / p.max_rts % p.num_kv_heads, e.x,
                   min(ROWS, (s.q_len << p.group_shift) - rt * ROWS));
   }
+  auto piece_of = [&](int c) { return static_cast<size_t>(c) * 2 + (c == e.z ? 1 : 0); };
+  auto output_of = [&](int c, int r) {
+    return reinterpret_cast<const float4*>(
+        p.ws_o)[((piece_of(c) * (D / 8) + c4 / 2) * ROWS + r) * 2 + c4 % 2];
+  };
   for (int r0 = static_cast<int>(blockIdx.y) * RB; r0 < e.w; r0 += RB * gridDim.y) {
     const int r = r0 + t / (D / 4);
     float big = -INFINITY, num[4] = {}, den = 0.f;
@@ -1290,10 +1295,8 @@ __global__ void __launch_bounds__(kTreeMergeThreads, SLICES > 1 ? 1 : 8)
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const int c = min(c0 + i * SLICES, last);
-          const size_t piece = static_cast<size_t>(c) * 2 + (c == e.z ? 1 : 0);
-          ml[i] = p.ws_ml[piece * ROWS + r];
-          o[i] = reinterpret_cast<const float4*>(
-              p.ws_o)[((piece * (D / 8) + c4 / 2) * ROWS + r) * 2 + c4 % 2];
+          ml[i] = p.ws_ml[piece_of(c) * ROWS + r];
+          o[i] = output_of(c, r);
         }
 #pragma unroll
         for (int i = 0; i < N; ++i)
@@ -1313,6 +1316,24 @@ __global__ void __launch_bounds__(kTreeMergeThreads, SLICES > 1 ? 1 : 8)
             make_float4(part[k][2][t], part[k][3][t], part[k][4][t], part[k][5][t]));
     }
     if (r >= e.w) continue;
+    // A piece's infinity is V's own and stays, however small the piece's weight: where
+    // a weight of 0 made it NaN, the element is the sum of the pieces' non-finite ones.
+    const float any = (num[0] + num[1]) + (num[2] + num[3]);
+    if (any != any && den == den) {
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int c = e.z; c <= last; ++c) {
+        const float4 o = output_of(c, r);
+        if (!(fabsf(o.x) < INFINITY)) sum.x += o.x;
+        if (!(fabsf(o.y) < INFINITY)) sum.y += o.y;
+        if (!(fabsf(o.z) < INFINITY)) sum.z += o.z;
+        if (!(fabsf(o.w) < INFINITY)) sum.w += o.w;
+      }
+      if (num[0] != num[0]) num[0] = sum.x;
+      if (num[1] != num[1]) num[1] = sum.y;
+      if (num[2] != num[2]) num[2] = sum.z;
+      if (num[3] != num[3]) num[3] = sum.w;
+    }
     const float inv = den > 0.f || den != den ? 1.f / den : 0.f;
     T* out = static_cast<T*>(p.out) +
              (static_cast<size_t>(e.x + (r >> p.group_shift)) * p.num_heads +
