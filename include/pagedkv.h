@@ -597,8 +597,9 @@ pkv_status pkv_paged_attn_decode_cascade_fp8(
  * accumulation; output rounded to nearest even.  A key's weight is rounded on its
  * way to V: over fp16 and E4M3 caches to fp16, off by at most 2^-11 of itself, or
  * 2^-32 of the row's largest weight where that is more; over bf16 caches by at most
- * 2^-17 of itself.  K and V of nodes that a row
- * does not see do not enter it, whatever they hold (NaN and infinities too).
+ * 2^-17 of itself.  K and V of nodes that a row does not see do not enter it,
+ * whatever they hold (NaN and infinities too); where a row sees NaN or infinities
+ * in V, the element is their sum, whatever their weight.
  * A chain (parents[j] = j - 1) is pkv_paged_attn_prefill's causal mask; one
  * node per sequence is pkv_paged_attn_decode.
  *

@@ -49,7 +49,8 @@
 // per unit by following the parents.  What a row does not see must not enter
 // it, and 0 x NaN would: K is masked in S, and non-finite elements of the
 // tree's V are taken out of the tile (and added to the rows that do see them
-// when the output is written).  Rows of V past the context are zeroed.
+// when the output is written).  Rows of V past the context are zeroed.  Rows of O that
+// hold a NaN are looked at again (tree_non_finite): an infinity stays one.
 //
 // Every wait is bounded; a role that gives up reports PKV_DEVERR_TIMEOUT, and
 // TMEM is freed on every path.
@@ -304,6 +305,63 @@ struct TreeTraits {
   static_assert(MIN_BLOCKS * (1024 + 1024 + SMEM) <= 228 * 1024, "shared memory per SM");
   static size_t smem_bytes() { return 1024 + static_cast<size_t>(SMEM); }
 };
+
+// Infinities and NaN in the V of visible keys k0 .. k1 - 1: where a warp's rows see any,
+// their sum is the element's value, whatever the rest is.  Those of the tree (keys from
+// `hist`; `seen`: the row's visible nodes, or null) were taken out of the tile; one of the
+// history, where its weight, or a bf16 half of it, is 0 or negative, made NaN of O.
+// `out`, or the piece `ws`, is this lane's row (or both are null).  For 16-bit caches
+// (E4M3 has no infinities); called by whole warps, and not inline: inline it cost the GQA
+// chat batch 62.5 -> 74.8 us, so 65.0.
+template <class T, int D, int ROWS>
+__device__ __noinline__ void tree_non_finite(const void* v_cache, const int32_t* table,
+                                             int num_blocks, int num_kv_heads, int kvh,
+                                             int block_size, int hist, int k0, int k1,
+                                             bool history, const uint32_t* seen, T* out,
+                                             float* ws) {
+  constexpr int PER = D / 32;  // a lane's dims
+  const int lane = threadIdx.x & 31;
+  // f(e, value) for the non-finite elements of a key in dims d0 + e, e < dims
+  auto odd_of = [&](int key, int d0, int dims, auto f) {
+    const int pb = table[key / block_size];
+    if (static_cast<unsigned>(pb) >= static_cast<unsigned>(num_blocks)) return;
+    const size_t at =
+        ((static_cast<size_t>(pb) * num_kv_heads + kvh) * block_size + key % block_size) * D + d0;
+#pragma unroll
+    for (int e = 0; e < dims; ++e) {
+      const float x = static_cast<float>(static_cast<const T*>(v_cache)[at + e]);
+      if (!(fabsf(x) < INFINITY)) f(e, x);
+    }
+  };
+  float hsum[PER] = {};  // of the history, which every row sees
+  if (history) {
+#pragma unroll 8
+    for (int key = k0; key < min(hist, k1); ++key)
+      odd_of(key, lane * PER, PER, [&](int e, float x) { hsum[e] += x; });
+  }
+#pragma unroll 1
+  for (int src = 0; src < 32; ++src) {
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const int c = src * PER + e;
+      float sum = __shfl_sync(kFullMask, hsum[e], src);
+      if (seen != nullptr) {
+#pragma unroll 1
+        for (int n = max(0, k0 - hist); n < k1 - hist; ++n)
+          if (seen[n >> 5] >> (n & 31) & 1u)
+            odd_of(hist + n, c, 1, [&](int, float x) { sum += x; });
+      }
+      if (sum == 0.f || (out == nullptr && ws == nullptr)) continue;
+      float* to = ws + static_cast<size_t>(c / 8) * ROWS * 8 + c % 8;
+      const float o = out != nullptr ? static_cast<float>(out[c]) : *to;
+      if (!history && !(fabsf(o) < INFINITY)) sum += o;  // the history's infinity
+      if (out != nullptr)
+        out[c] = static_cast<T>(sum);
+      else
+        *to = sum;
+    }
+  }
+}
 
 template <class Tr>
 __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
@@ -1055,9 +1113,11 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
       const size_t row = row_at(it, qt, min(r, nrows - 1));
       // pieces: the one that starts a unit is its CTA's second, any other its first
       const size_t piece = static_cast<size_t>(blockIdx.x) * 2 + (it.t0 == 0 ? 1 : 0);
+      bool from_history = false;
       if (warp_active) {
         const float inv = l > 0.f || l != l ? v_scale / l : 0.f;
         if (!whole && active) p.ws_ml[piece * ROWS + qt * M + r] = make_float2(l != l ? l : m, l);
+        float top = 0.f;  // NaN if an element is
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float v[32];
@@ -1070,6 +1130,11 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
             for (int i = 0; i < 32; ++i) v[i] = v[i] * f0 + x[i] * f1;
           } else {
             tc::tmem_wait_ld();
+          }
+          if constexpr (!Tr::kFp8) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              asm("max.NaN.f32 %0, %1, %2, %0;" : "+f"(top) : "f"(v[i]), "f"(v[i + 1]));
           }
           if (!active) continue;
           if (whole) {
@@ -1100,15 +1165,23 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
             }
           }
         }
+        if constexpr (!Tr::kFp8) from_history = __any_sync(kFullMask, active && l == l && top != top);
       }
-      if (odd && active && l == l) {
-        // infinities and NaN in the V of the nodes that this row sees: their sum
-        // is the element's value, whatever the rest is
-        const int32_t* trow = p.block_tables + static_cast<size_t>(it.seq) * p.max_blocks_per_seq;
+      const int32_t* trow = p.block_tables + static_cast<size_t>(it.seq) * p.max_blocks_per_seq;
+      const bool mine = active && l == l;  // a row whose sum is NaN stays NaN
+      if constexpr (!Tr::kFp8) {
+        if (odd || from_history)
+          tree_non_finite<T, D, ROWS>(
+              p.v_cache, trow, p.num_blocks, p.num_kv_heads, it.kvh, p.block_size, hist,
+              it.t0 * NKEY, min(it.ctx, it.t1 * NKEY), from_history, odd && mine ? seen : nullptr,
+              mine && whole ? static_cast<T*>(p.out) + row * D : nullptr,
+              mine && !whole ? p.ws_o + (piece * (D / 8) * ROWS + qt * M + r) * 8 : nullptr);
+      } else if (odd && mine) {
+        // NaN in the V of the nodes that this row sees (the history's is in O)
         const int lo = max(0, it.t0 * NKEY - hist), hi = min(it.q_len, it.t1 * NKEY - hist);
 #pragma unroll 1
         for (int c = 0; c < D; ++c) {
-          float sum = 0.f;
+          bool nan = false;
 #pragma unroll 1
           for (int n = lo; n < hi; ++n) {
             if (!(seen[n >> 5] >> (n & 31) & 1u)) continue;
@@ -1117,18 +1190,13 @@ __global__ void __launch_bounds__(Tr::THREADS, Tr::MIN_BLOCKS)
             if (static_cast<unsigned>(pb) >= static_cast<unsigned>(p.num_blocks)) continue;
             const size_t at = ((static_cast<size_t>(pb) * p.num_kv_heads + it.kvh) *
                                    p.block_size + key % p.block_size) * D + c;
-            float x;
-            if constexpr (Tr::kFp8)
-              x = (static_cast<const uint8_t*>(p.v_cache)[at] & 0x7F) == 0x7F ? NAN : 0.f;
-            else
-              x = static_cast<float>(static_cast<const T*>(p.v_cache)[at]);
-            if (!(fabsf(x) < INFINITY)) sum += x;
+            nan |= (static_cast<const uint8_t*>(p.v_cache)[at] & 0x7F) == 0x7F;
           }
-          if (sum == 0.f) continue;
+          if (!nan) continue;
           if (whole)
-            static_cast<T*>(p.out)[row * D + c] = static_cast<T>(sum);
+            static_cast<T*>(p.out)[row * D + c] = static_cast<T>(NAN);
           else
-            p.ws_o[((piece * (D / 8) + c / 8) * ROWS + qt * M + r) * 8 + c % 8] = sum;
+            p.ws_o[((piece * (D / 8) + c / 8) * ROWS + qt * M + r) * 8 + c % 8] = NAN;
         }
       }
       tc::tc_fence_before();

@@ -71,3 +71,82 @@ def test_infinite_v_of_a_node_in_a_piece_of_no_weight(pk, dtype, fp8, heads, d, 
             else:
                 close(got[n, :1, dims], ref[n, :1, dims], mag[n, :1, dims], dtype)
         close(got[n, :1, 3::4], ref[n, :1, 3::4], mag[n, :1, 3::4], dtype)
+
+
+# whole and cut units; one query tile, two in turn, two side by side
+@pytest.mark.parametrize("hist,nodes,heads,d", [
+    ([300], [8], 8, 128), ([70, 20], [40, 24], 2, 64), ([6000, 130], [5, 3], 4, 128),
+    ([3000, 50], [64, 20], 16, 128), ([3000] * 30, [9] * 30, 8, 64)])
+@pytest.mark.parametrize("dtype,fp8", [("fp16", False), ("bf16", False), ("fp16", True)])
+def test_infinite_v_in_the_history(pk, hist, nodes, heads, d, dtype, fp8):
+    w = tree_workload(hist, nodes, heads, 2, d, 16, dtype, seed=62)
+    t = TreeOnDevice(pk, w, scales=([0.0125, 0.02], [0.01, 0.03]) if fp8 else None)
+    first = int(w.query_start[1]) - 1
+    rows = {(0, 0), (first, heads - 1), (first // 2, heads // 2)}
+    if len(nodes) > 1:
+        rows |= {(first + 1, 0), (len(w.q) - 1, heads - 1)}
+    ref, mag = t.reference(rows)
+    inf, minus, nan = special(dtype, fp8)
+    h = hist[0]
+    for pos, dims, what in ((0, 0, inf), (h - 1, 1, minus), (h // 2, 2, nan), (h // 3, 3, inf),
+                            (h // 3 + 9, 3, minus), (h // 5, 4, inf), (h - 2, 4, inf)):
+        put(t, w, 0, pos, slice(dims, None, 8), what)
+    t.upload()
+    assert t.run() == 0
+    got = widen_out(dev_to_bits(t.out), w)
+    own = got[:first + 1]
+    for dims, what in ((0, np.isposinf), (1, np.isneginf), (2, np.isnan), (3, np.isnan),
+                       (4, np.isposinf)):
+        assert (np.isnan if fp8 else what)(own[:, :, dims::8]).all(), dims
+    assert np.isfinite(own.reshape(-1, heads, d // 8, 8)[..., 5:]).all()
+    assert np.isfinite(got[first + 1:]).all()
+    for n, head in rows:
+        at = np.arange(d) % 8 >= (5 if n <= first else 0)
+        close(got[n, head, at], ref[n, head, at], mag[n, head, at], dtype)
+
+
+# the infinity's weight underflows: far below the row's maximum, before and behind it
+@pytest.mark.parametrize("hist,nodes,heads", [(700, 5, 4), (9000, 5, 4), (2000, 64, 16)])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("peak", [0.1, 0.9])
+def test_infinite_v_of_no_weight_in_the_history(pk, hist, nodes, heads, dtype, peak):
+    d = 128
+    w = tree_workload([hist], [nodes], heads, 2, d, 16, dtype, seed=63)
+    w.q = np.broadcast_to(bits(1.0, dtype), w.q.shape).copy()
+    low = bits(-150.0 / (w.scale * d), dtype)
+    w.k_cache[:] = low
+    w.key[:] = low
+    at = int(hist * peak)
+    w.k_cache[w.block_tables[0, at // 16], :, at % 16] = bits(0.0, dtype)
+    t = TreeOnDevice(pk, w)
+    inf, minus, nan = special(dtype, False)
+    for pos, dims, what in ((5, 0, inf), (hist // 2, 1, minus), (hist - 3, 2, inf),
+                            (at, 3, minus)):
+        put(t, w, 0, pos, slice(dims, None, 8), what)
+    t.upload()
+    assert t.run() == 0
+    got = widen_out(dev_to_bits(t.out), w)
+    for dims, what in ((0, np.isposinf), (1, np.isneginf), (2, np.isposinf), (3, np.isneginf)):
+        assert what(got[:, :, dims::8]).all(), dims
+    assert np.isfinite(got.reshape(-1, heads, d // 8, 8)[..., 4:]).all()
+
+
+@pytest.mark.parametrize("hist,nodes,heads", [(300, 8, 8), (9000, 6, 4), (3000, 64, 16)])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_opposite_infinities_in_history_and_tree(pk, hist, nodes, heads, dtype):
+    w = tree_workload([hist], [nodes], heads, 2, 64, 16, dtype, seed=64, kind="chain")
+    t = TreeOnDevice(pk, w)
+    inf, minus, _ = special(dtype, False)
+    for base in (0, hist - 1):      # the first tile, and the one that the tree starts in
+        put(t, w, 0, base, slice(0, None, 8), inf)
+        put(t, w, 0, base, slice(1, None, 8), minus)
+    put(t, w, 0, hist + 3, slice(0, None, 8), minus)
+    put(t, w, 0, hist + 3, slice(1, None, 8), minus)
+    put(t, w, 0, hist + 3, slice(2, None, 8), inf)
+    t.upload()
+    assert t.run() == 0
+    got = widen_out(dev_to_bits(t.out), w)
+    assert np.isposinf(got[:3, :, 0::8]).all() and np.isnan(got[3:, :, 0::8]).all()
+    assert np.isneginf(got[:, :, 1::8]).all()
+    assert np.isfinite(got[:3, :, 2::8]).all() and np.isposinf(got[3:, :, 2::8]).all()
+    assert np.isfinite(got.reshape(nodes, heads, 8, 8)[..., 3:]).all()
