@@ -25,11 +25,11 @@ and copy them on write ([cortexgrid] FAQ on parallel sampling).
 4. fork the samples of a request whose prompt was just prefilled, retire
    sequences that reached their output length, free their pages.
 
-With a ``drafter`` the running sequences decode speculatively: step 2 reserves a
-slot for every node of the tree that the drafter proposes for a sequence, step 3
-attends with ``paged_attn_tree``, verifies with ``verify_draft`` and moves the
-kept nodes' K/V together with ``compact_accepted``, and step 4 cuts the sequence
-back to what was kept (at least the tree's root, the token sampled last).
+With a ``drafter`` the running sequences decode speculatively: before step 1 the
+drafter proposes a tree for each of them; step 2 reserves a slot for every
+node, step 3 attends with ``paged_attn_tree``, verifies with ``verify_draft`` and
+moves the kept nodes' K/V together with ``compact_accepted``, and step 4 cuts the
+sequence back to what was kept (at least the tree's root, the token sampled last).
 
 Queries, keys and values are synthetic (seeded N(0,1)), and so are a drafted
 step's probabilities and uniforms: the driver exercises the memory manager and
@@ -130,9 +130,15 @@ class ContinuousBatcher:
     # -- one iteration ---------------------------------------------------------
     def step(self):
         alloc = self.alloc
+        # a drafted step's trees come first: nothing has changed if the drafter fails
+        decoded = list(self.running)
+        trees = []
+        if self.drafter is not None and decoded:
+            hist = alloc.context_lens(decoded)
+            trees = [self._tree(sid, n) for sid, n in zip(decoded, hist)]
         # 1. admission, in arrival order
         admitted = []
-        budget = self.max_batched - len(self.running) * (self.max_draft if self.drafter else 1)
+        budget = self.max_batched - len(decoded) * (self.max_draft if self.drafter else 1)
         while self.waiting:
             req = self.waiting[0]
             if req.arrival > self.step_index:
@@ -159,14 +165,9 @@ class ContinuousBatcher:
             admitted.append((sid, req))
         # 2. one new slot per running sequence, or per node of its tree (CoW pairs for
         #    shared partial blocks)
-        decoded = list(self.running)
-        slots_dec, pairs, trees = [], [], []
+        slots_dec, pairs = [], []
         if decoded:
-            owners = decoded
-            if self.drafter is not None:
-                hist = alloc.context_lens(decoded)
-                trees = [self._tree(sid, n) for sid, n in zip(decoded, hist)]
-                owners = [sid for sid, t in zip(decoded, trees) for _ in t]
+            owners = [sid for sid, t in zip(decoded, trees) for _ in t] if trees else decoded
             try:
                 slots_dec, pairs = alloc.append_slots(owners)
             except pk.PagedKVError as e:
