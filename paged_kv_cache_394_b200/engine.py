@@ -147,10 +147,18 @@ class ContinuousBatcher:
                 break
             if req.prompt_len > budget:
                 break
-            # keep the blocks that the running sequences may take in this step
+            # keep the blocks that the running sequences may take in this step and, drafting,
+            # those that the admitted ones' first trees may take in the next; a request that
+            # has the pool to itself gets what there is
             need = -(-req.prompt_len // self.bs)
-            if alloc.num_free() < need + (len(self.running) * self.step_blocks
-                                          + len(admitted) * req.samples):
+            if self.drafter is None:
+                keep = len(self.running) + len(admitted) * req.samples
+            elif decoded or admitted:
+                keep = self.step_blocks * (len(decoded) + req.samples
+                                           + sum(r.samples for _, r in admitted))
+            else:
+                keep = 0
+            if alloc.num_free() < need + keep:
                 break
             sid = self.next_seq
             try:

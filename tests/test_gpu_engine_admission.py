@@ -1,4 +1,5 @@
-"""Admission beside drafted steps: a drafter that fails."""
+"""Admission beside drafted steps: blocks kept for the trees of what was just
+admitted, and a drafter that fails."""
 
 import pytest
 
@@ -19,6 +20,37 @@ def request(arrival, prompt, output, samples=1):
     from paged_kv_cache_394_b200 import engine as E
 
     return E.Request(0, prompt, output, arrival=arrival, samples=samples)
+
+
+# two requests of a block each, whose trees take two blocks more each: 6 blocks in all
+@pytest.mark.parametrize("blocks,together", [(5, False), (6, False), (8, True)])
+def test_a_tight_pool_keeps_blocks_for_the_first_trees(blocks, together):
+    b = batcher(blocks, lambda sid, n: chain(32), max_draft=32, max_model_len=64)
+    for _ in range(2):
+        b.submit(request(0, 16, 8))
+    at_once = 0
+    for _ in range(40):
+        rec = b.step()
+        at_once = max(at_once, len(rec.decoded))
+        if b.idle():
+            break
+    assert b.idle() and b.alloc.num_free() == blocks
+    assert at_once == (2 if together else 1)
+
+
+def test_blocks_are_kept_for_every_sample():
+    # the first trees of 4 sequences may take 3 blocks each, and 13 are free, 2 of them
+    # for the second prompt
+    b = batcher(15, lambda sid, n: chain(32), max_draft=32, max_model_len=64)
+    b.submit(request(0, 20, 6, samples=3))
+    b.submit(request(0, 20, 6))
+    first = b.step()
+    assert len(first.admitted) == 1 and len(first.forked) == 2
+    for _ in range(40):
+        b.step()
+        if b.idle():
+            break
+    assert b.idle() and b.alloc.num_free() == 15
 
 
 @pytest.mark.parametrize("bad", [[0], [-1, 1], [], [-1] + [0] * 40, None])
