@@ -26,7 +26,8 @@ and copy them on write ([cortexgrid] FAQ on parallel sampling).
    sequences that reached their output length, free their pages.
 
 With a ``drafter`` the running sequences decode speculatively: before step 1 the
-drafter proposes a tree for each of them; step 2 reserves a slot for every
+drafter proposes a tree for each of them, cut so that all trees together keep to
+max_num_batched_tokens (a root each at least); step 2 reserves a slot for every
 node, step 3 attends with ``paged_attn_tree``, verifies with ``verify_draft`` and
 moves the kept nodes' K/V together with ``compact_accepted``, and step 4 cuts the
 sequence back to what was kept (at least the tree's root, the token sampled last).
@@ -132,13 +133,15 @@ class ContinuousBatcher:
         alloc = self.alloc
         # a drafted step's trees come first: nothing has changed if the drafter fails
         decoded = list(self.running)
-        trees = []
+        trees, per_seq = [], 1
         if self.drafter is not None and decoded:
+            # nodes of all trees within the token budget, at least the root of each
+            per_seq = min(self.max_draft, max(1, self.max_batched // len(decoded)))
             hist = alloc.context_lens(decoded)
-            trees = [self._tree(sid, n) for sid, n in zip(decoded, hist)]
+            trees = [self._tree(sid, n, per_seq) for sid, n in zip(decoded, hist)]
         # 1. admission, in arrival order
         admitted = []
-        budget = self.max_batched - len(decoded) * (self.max_draft if self.drafter else 1)
+        budget = self.max_batched - len(decoded) * per_seq
         while self.waiting:
             req = self.waiting[0]
             if req.arrival > self.step_index:
@@ -289,14 +292,14 @@ class ContinuousBatcher:
                           next_tokens=sampled.tolist() if trees else [])
 
     # -- drafts ------------------------------------------------------------------
-    def _tree(self, sid, context_len):
-        """The sequence's tree, cut to what max_model_len leaves room for."""
+    def _tree(self, sid, context_len, limit):
+        """The sequence's tree, cut to ``limit`` nodes and what max_model_len leaves room for."""
         parents = [int(x) for x in self.drafter(sid, context_len)]
         if not 1 <= len(parents) <= self.max_draft:
             raise ValueError("a tree must have 1 .. max_draft nodes")
         if parents[0] != -1 or any(not 0 <= x < j for j, x in enumerate(parents) if j):
             raise ValueError("a tree has one root, and parents before their nodes")
-        return parents[:self.max_model_len - context_len]
+        return parents[:min(limit, self.max_model_len - context_len)]
 
     def _synthetic_draws(self, parents, query_start):
         t, v = parents.numel(), self.vocab

@@ -1,5 +1,5 @@
 """Admission beside drafted steps: blocks kept for the trees of what was just
-admitted, and a drafter that fails."""
+admitted, a drafter that fails, and the token budget."""
 
 import pytest
 
@@ -83,3 +83,24 @@ def test_a_failing_drafter_loses_no_request(bad):
     while not b.idle():
         b.step()
     assert b.alloc.num_free() == 40
+
+
+@pytest.mark.parametrize("budget,most", [(40, 5), (8, 1), (6, 1), (400, 16)])
+def test_trees_keep_to_the_token_budget(budget, most):
+    b = batcher(200, lambda sid, n: chain(16), max_draft=16, max_num_batched_tokens=budget,
+                max_model_len=64)
+    for _ in range(8):
+        b.submit(request(0, 5, 12))
+    eight = 0
+    while not b.idle():
+        rec = b.step()
+        if len(rec.decoded) == 8:
+            eight += 1
+            assert [len(t) for t in rec.parents] == [most] * 8
+        if rec.decoded:
+            drafted = sum(len(t) for t in rec.parents)
+            assert drafted <= max(budget, len(rec.decoded))
+            assert drafted + rec.prefill_tokens <= max(budget, len(rec.decoded))
+        assert all(1 <= k <= len(t) for k, t in zip(rec.kept, rec.parents))
+    assert eight > 0 or budget < 40
+    assert b.alloc.num_free() == 200
