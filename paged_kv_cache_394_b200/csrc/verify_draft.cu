@@ -276,15 +276,11 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
       if (c < x.f1) {
         if (taken == 0.0) {
           whole(std::false_type(), [&](float a, float) { s += static_cast<double>(a); });
-        } else if (taken == 1.0) {
-          // a - b for a > b as a float and its exact error: one conversion
-          float low = 0.f;
+        } else if (taken == 1.0) {  // a node's first rejection: no product
           whole(std::true_type(), [&](float a, float b) {
-            const float d = fmaxf(a - b, 0.f);
-            s += static_cast<double>(d);
-            if (d > 0.f && d < INFINITY) low += (a - d) - b;
+            const double d = static_cast<double>(a) - static_cast<double>(b);
+            if (d > 0.0) s += d;
           });
-          s += static_cast<double>(low);
         } else {
           whole(std::true_type(), [&](float a, float b) { s += residual(a, b, taken); });
         }
