@@ -52,7 +52,7 @@ bool tree_whole(long long units, int max_context_len) {
 // can have more than 128 rows, as its query tiles share each K/V tile; over E4M3,
 // whose tiles, held twice, leave room for one CTA an SM; for whole units that are no
 // more than the SMs, as the groups take a unit's tiles in turn (1 sequence of 300
-// tokens 10.1 -> 8.9 us, 16 of 700 16.8 -> 15.0); and from 64 rows a unit, where the
+// tokens 10.1 -> 8.9 us, 16 of 700 16.8 -> 15.0); and above 64 rows a unit, where the
 // deeper ring of tiles outlasts a unit's change (GQA chat batch 69 -> 66).  Else one
 // query tile and two CTAs an SM (LLaMA-7B batch, 16 rows a unit: 163 -> 105 us; 64
 // sequences of 700 tokens, 32 rows: 59 -> 43).
@@ -141,7 +141,6 @@ pkv_status tree_launch(void* out, const void* q, const void* k_cache, const void
   TreeParams p = {};
   p.out = out;
   p.q = q;
-  p.k_cache = k_cache;
   p.v_cache = v_cache;
   p.block_tables = block_tables;
   p.context_lens = context_lens;

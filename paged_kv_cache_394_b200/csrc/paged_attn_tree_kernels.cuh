@@ -69,8 +69,7 @@ namespace pkv {
 struct TreeParams {
   void* out;
   const void* q;
-  const void* k_cache;
-  const void* v_cache;
+  const void* v_cache;  // for non-finite elements; K and V come through the tensor maps
   const int32_t* block_tables;
   const int32_t* context_lens;
   const int32_t* query_start;
@@ -87,9 +86,9 @@ struct TreeParams {
   unsigned* err;
   // Workspace: for each CTA one merge entry and two pieces of ROWS rows.  Entry c
   // is of the unit that ended in CTA c, {first token, kv head, first CTA, rows},
-  // rows = 0 where none did that another CTA began; or, with no more units than
-  // CTAs (by_unit), entry u is of unit u (of max_rts for every (sequence, kv head)),
-  // {first CTA, last CTA}, the same one where the unit is not cut.
+  // rows = 0 where none did that another CTA began; or, with at least 8 CTAs a unit
+  // (by_unit: units in many pieces), entry u is of unit u (of max_rts for every
+  // (sequence, kv head)), {first CTA, last CTA}, the same one where it is not cut.
   int by_unit;
   int4* ws_meta;
   float2* ws_ml;  // (max, sum) of each row of each piece

@@ -21,8 +21,9 @@
 // loads), so that all of them walk alike; each warp of the cluster has its own
 // contiguous piece of the vocabulary.
 // A pass leaves a sum per warp; the CTAs exchange theirs through distributed
-// shared memory, and only the warp whose piece holds the next token reads that
-// piece again.  All sums are 64-bit and in a fixed order.
+// shared memory, and only the piece that holds the next token is read again: all
+// warps of its CTA sum a share of it, and one scans the share that holds the token.
+// All sums are 64-bit and in a fixed order.
 #include <cooperative_groups.h>
 #include <math.h>
 
