@@ -311,7 +311,7 @@ struct TreeTraits {
 // history, where its weight, or a bf16 half of it, is 0 or negative, made NaN of O.
 // `out`, or the piece `ws`, is this lane's row (or both are null).  For 16-bit caches
 // (E4M3 has no infinities); called by whole warps, and not inline: inline it cost the GQA
-// chat batch 62.5 -> 74.8 us, so 65.0.
+// chat batch 62.5 -> 74.8 us, so 65.0.  Where there are any it takes 0.3 us a key.
 template <class T, int D, int ROWS>
 __device__ __noinline__ void tree_non_finite(const void* v_cache, const int32_t* table,
                                              int num_blocks, int num_kv_heads, int kvh,

@@ -358,10 +358,12 @@ def fp8_scales(scales, num_kv_heads, device=None):
 
 
 def _scales_for(k_scales, v_scales, hkv, device, stream):
-    ks, vs = fp8_scales(k_scales, hkv, device), fp8_scales(v_scales, hkv, device)
-    if stream is not None:   # a temporary must outlive the launch on that stream
-        ks.record_stream(stream)
-        vs.record_stream(stream)
+    if stream is None:
+        return fp8_scales(k_scales, hkv, device), fp8_scales(v_scales, hkv, device)
+    with torch.cuda.stream(stream):   # a number is filled in before the launch on that stream
+        ks, vs = fp8_scales(k_scales, hkv, device), fp8_scales(v_scales, hkv, device)
+    ks.record_stream(stream)
+    vs.record_stream(stream)
     return ks, vs
 
 
